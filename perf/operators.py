@@ -1,0 +1,372 @@
+"""What is measured of the routing, dense-product and routed-experts operators.
+
+Three operators that stand around the MoE layer's own kernels:
+
+* ``route``: scored routing of router logits [T, E] -- softmax or sigmoid scores, a bias that
+  takes part in the choice only, a choice limited to the best groups of experts, top-k with ties
+  to the lower index, renormalised and scaled weights; unavailable slots are -1 with weight 0.
+* ``linear``: act(x w^T + b) [* (x w_up^T + b_up)] [+ residual], bf16 in, bf16 or fp32 out.
+* ``experts``: the experts' products on a routing that is given: sum_j w_tj FFN_{idx_tj}(x_t).
+
+``run`` computes them in elementary torch operations, or, where ``own`` is true, by the calls a
+user of ``routed_grouped_gemm_softmax_b200.api`` makes.  ``exact`` computes them in 64 bits, written apart.
+"""
+import math
+
+import torch
+
+own = False
+
+F32_MAX = torch.finfo(torch.float32).max
+
+
+# ------------------------------------------------------------------ cases
+
+def _route(name, T, E, k, score, bias, groups, group_k, group_score, renorm, scale, logits, mask, pad):
+    return {"name": name, "op": "route", "T": T, "E": E, "k": k, "score": score, "bias": bias, "groups": groups,
+            "group_k": group_k, "group_score": group_score, "renorm": renorm, "scale": scale, "logits": logits,
+            "mask": mask, "pad": pad}
+
+
+def _linear(name, M, N, K, act, bias, residual, gated, out, pad):
+    return {"name": name, "op": "linear", "M": M, "N": N, "K": K, "act": act, "bias": bias, "residual": residual,
+            "gated": gated, "out": out, "pad": pad}
+
+
+def _experts(name, T, H, I, E, k, empty):
+    return {"name": name, "op": "experts", "T": T, "H": H, "I": I, "E": E, "k": k, "empty": empty}
+
+
+def listed():
+    return [
+        # one decode step's 16 tokens, sigmoid scores with a balance bias, 4 of 8 groups: a call's latency
+        _route("route decode", 16, 256, 8, "sigmoid", True, 8, 4, "top2", True, 2.5, "f32", "none", 0),
+        # a prefill batch with the same router, its last rows padding (no expert available)
+        _route("route prefill padded", 4096, 256, 8, "sigmoid", True, 8, 4, "top2", True, 2.5, "f32", "padded", 0),
+        # a long batch, softmax over all experts, plain top-6 of 64, bf16 logits (many ties)
+        _route("route long softmax", 65536, 64, 6, "softmax", False, 1, 1, "max", False, 1.0, "bf16", "none", 0),
+        # an odd expert count in groups limited by their best expert, masked experts, rows of a wider buffer
+        _route("route odd masked", 8191, 160, 6, "softmax", False, 8, 3, "max", False, 16.0, "f32", "experts", 5),
+        # one token through an output projection with its residual: a weight stream, latency
+        _linear("linear one token", 1, 2048, 2048, "none", False, True, False, "bf16", 0),
+        # a decode batch through the gated half of a dense SwiGLU layer
+        _linear("linear decode gated", 16, 2048, 7168, "silu", False, False, True, "bf16", 0),
+        # router logits of a prefill batch, kept in fp32
+        _linear("linear router logits", 4096, 256, 2048, "none", True, False, False, "f32", 0),
+        # ragged sizes: rows, columns and depth that no tile divides, padded row strides
+        _linear("linear ragged gelu", 1001, 4099, 1416, "gelu", True, True, False, "bf16", 8),
+        # a dense gated layer of a long batch
+        _linear("linear large gated", 8192, 5632, 4096, "silu", False, False, True, "bf16", 0),
+        # its down product onto the residual stream
+        _linear("linear large down", 8192, 4096, 5632, "none", True, True, False, "bf16", 0),
+        # a decode step's experts on a given routing
+        _experts("experts decode", 16, 2048, 512, 256, 8, 0.0),
+        # a prefill batch with padded rows that no expert takes
+        _experts("experts prefill padded", 2048, 2048, 512, 64, 6, 0.125),
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(["route", "linear", "linear", "experts"])
+    if op == "route":
+        E, groups, group_k = rng.choice([(8, 1, 1), (60, 4, 2), (64, 1, 1), (64, 8, 3), (96, 1, 1), (128, 4, 2), (160, 8, 3),
+                                         (256, 8, 4), (256, 1, 1), (384, 1, 1), (512, 16, 4), (1000, 1, 1)])
+        k = min(rng.choice([1, 2, 4, 6, 8, 10]), E * group_k // groups)
+        T = _log(rng, 1, min(65536, (65536 * 64) // E))
+        score = rng.choice(["softmax", "sigmoid"])
+        c = _route("", T, E, k, score, rng.random() < 0.5, groups, group_k, rng.choice(["max", "top2"]),
+                   rng.random() < 0.5, rng.choice([1.0, 2.5]), rng.choice(["f32", "bf16"]),
+                   rng.choice(["none", "padded", "experts"]), rng.choice([0, 0, 3, 8]))
+    elif op == "linear":
+        M, N, K = _log(rng, 1, 8192), _log(rng, 8, 8192), 8 * _log(rng, 8, 900)
+        gated = rng.random() < 0.3
+        out = "bf16" if rng.random() < 0.75 else "f32"
+        c = _linear("", M, N, K, rng.choice(["none", "relu", "silu", "gelu", "gelu_tanh"]), rng.random() < 0.5,
+                    rng.random() < 0.5, gated, out, rng.choice([0, 0, 8, 24]))
+        if 2 * M * N * K * (2 if gated else 1) > 2 * 8192 * 5632 * 4096 * 2:
+            c["gated"] = False
+    else:
+        H, I, E = 64 * _log(rng, 4, 32), 64 * _log(rng, 2, 16), rng.choice([8, 16, 60, 64])
+        c = _experts("", _log(rng, 1, 2048), H, I, E, rng.choice([1, 2, 4, 6, 8]), rng.choice([0.0, 0.125, 0.5]))
+    del c["name"]
+    return c
+
+
+# ------------------------------------------------------------------ inputs
+
+def _gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def _rows(n, cols, pad, dtype, gen, scale=1.0):
+    """[n, cols] normal values as rows of a buffer that is `pad` columns wider."""
+    buf = (torch.randn(n, cols + pad, generator=gen, device="cuda") * scale).to(dtype)
+    return buf[:, :cols]
+
+
+def prepare(case, seed):
+    g = _gen(seed)
+    s = dict(case)
+    if case["op"] == "route":
+        T, E = case["T"], case["E"]
+        dt = torch.float32 if case["logits"] == "f32" else torch.bfloat16
+        lift = 0.5 * torch.randn(E, generator=g, device="cuda")  # some experts are popular
+        buf = torch.randn(T, E + case["pad"], generator=g, device="cuda")
+        buf[:, :E] += lift
+        x = buf.to(dt)
+        if case["mask"] == "padded":
+            x[T - T // 8:] = -math.inf
+        elif case["mask"] == "experts":
+            u = torch.rand(T, E + case["pad"], generator=g, device="cuda")
+            rows = torch.rand(T, 1, generator=g, device="cuda")
+            x = torch.where(u < 0.1, torch.finfo(dt).min, x)
+            x = torch.where((u > 0.8) & (rows < 0.5), -math.inf, x)
+            x = torch.where((u > 0.02) & (rows > 0.95), -math.inf, x)  # rows with only a few experts left
+            x = torch.where((u > 0.79) & (u < 0.8) & (rows > 0.4), math.nan, x)
+        s["x"] = x[:, :E]
+        s["b"] = 0.05 * torch.randn(E, generator=g, device="cuda") if case["bias"] else None
+    elif case["op"] == "linear":
+        M, N, K, pad = case["M"], case["N"], case["K"], case["pad"]
+        bf, dt = torch.bfloat16, torch.bfloat16 if case["out"] == "bf16" else torch.float32
+        s["x"] = _rows(M, K, pad, bf, g)
+        s["w"] = _rows(N, K, pad, bf, g, K ** -0.5)
+        s["w_up"] = _rows(N, K, pad, bf, g, K ** -0.5) if case["gated"] else None
+        s["b"] = torch.randn(N, generator=g, device="cuda") if case["bias"] else None
+        s["b_up"] = torch.randn(N, generator=g, device="cuda") if case["bias"] and case["gated"] else None
+        s["r"] = _rows(M, N, pad, dt, g) if case["residual"] else None
+        if own:
+            from routed_grouped_gemm_softmax_b200 import api
+            s["ws"] = api.linear_workspace("cuda")  # the scratch a program keeps
+    else:
+        T, H, I, E, k = (case[n] for n in ("T", "H", "I", "E", "k"))
+        bf = torch.bfloat16
+        s["x"] = torch.randn(T, H, generator=g, device="cuda").to(bf)
+        s["w_gate"] = (torch.randn(E, I, H, generator=g, device="cuda") * H ** -0.5).to(bf)
+        s["w_up"] = (torch.randn(E, I, H, generator=g, device="cuda") * H ** -0.5).to(bf)
+        s["w_down"] = (torch.randn(E, H, I, generator=g, device="cuda") * I ** -0.5).to(bf)
+        u = torch.rand(T, E, generator=g, device="cuda") + 0.5 * torch.rand(E, generator=g, device="cuda")
+        s["idx"] = u.sort(dim=1, descending=True).indices[:, :k].to(torch.int32)  # distinct experts
+        w = torch.rand(T, k, generator=g, device="cuda") + 0.1
+        s["w"] = w / w.sum(dim=1, keepdim=True)
+        n = int(T * case["empty"])
+        if n:  # padded rows: no expert
+            s["idx"][T - n:] = -1
+            s["w"][T - n:] = 0.0
+        if own:
+            from routed_grouped_gemm_softmax_b200 import api
+            s["ws"] = api.workspace(T, H, I, E, k, "cuda")
+    return s
+
+
+# ------------------------------------------------------------------ the plain forms
+
+def _plain_route(s):
+    # the choice lies between near values, so the scores are taken in 64 bits
+    T, E, k, groups = s["T"], s["E"], s["k"], s["groups"]
+    x = s["x"].double()
+    ok = ~torch.isnan(x) & (x > -math.inf)
+    if s["b"] is not None:
+        ok = ok & (~torch.isnan(s["b"]) & (s["b"] > -math.inf))
+    x = torch.where(ok, x.clamp(max=F32_MAX), -math.inf)
+    if s["score"] == "sigmoid":
+        p = 1.0 / (1.0 + torch.exp(-x))
+    else:
+        m = x.amax(dim=1, keepdim=True)
+        e = torch.exp(x - torch.where(m == -math.inf, 0.0, m))
+        total = e.sum(dim=1, keepdim=True)
+        p = e / torch.where(total == 0, 1.0, total)
+    # without a bias the order of the scores is that of the logits
+    c = torch.where(ok, p + s["b"].double(), -math.inf) if s["b"] is not None else x
+    if groups > 1:
+        if s["group_score"] == "max":
+            gs = c.view(T, groups, E // groups).amax(dim=2)
+        else:
+            v = torch.where(ok, c if s["b"] is not None else p, -math.inf).view(T, groups, E // groups)
+            top = v.sort(dim=2, descending=True).values[:, :, :2]
+            gs = top[:, :, 0] + torch.where(top[:, :, 1:] > -math.inf, top[:, :, 1:], 0.0).sum(dim=2)
+        best = gs.sort(dim=1, descending=True, stable=True).indices[:, :s["group_k"]]
+        keep = torch.zeros(T, groups, dtype=torch.bool, device=x.device).scatter(1, best, True)
+        c = torch.where(keep.repeat_interleave(E // groups, dim=1), c, -math.inf)
+    val, idx = c.sort(dim=1, descending=True, stable=True)
+    val, idx = val[:, :k], idx[:, :k]
+    w = torch.where(val > -math.inf, p.gather(1, idx), 0.0)
+    if s["renorm"]:
+        total = w.sum(dim=1, keepdim=True)
+        w = w / torch.where(total == 0, 1.0, total)
+    return torch.where(val > -math.inf, idx, -1).to(torch.int32), (w * s["scale"]).float()
+
+
+def _act(v, act):
+    if act == "relu":
+        return torch.where(v < 0, 0.0, v)
+    if act == "silu":
+        return v / (1.0 + torch.exp(-v))
+    if act == "gelu":
+        return 0.5 * v * torch.erfc(v * -math.sqrt(0.5))
+    if act == "gelu_tanh":
+        return v / (1.0 + torch.exp(-2.0 * math.sqrt(2.0 / math.pi) * (v + 0.044715 * v * v * v)))
+    return v
+
+
+def _plain_linear(s):
+    x = s["x"].float()
+    v = x @ s["w"].float().t()
+    if s["b"] is not None:
+        v = v + s["b"]
+    v = _act(v, s["act"])
+    if s["w_up"] is not None:
+        u = x @ s["w_up"].float().t()
+        v = v * (u if s["b_up"] is None else u + s["b_up"])
+    if s["r"] is not None:
+        v = v + s["r"].float()
+    return v.to(torch.bfloat16) if s["out"] == "bf16" else v
+
+
+def _plain_experts(s):
+    # every expert on every token, each hidden row scaled by its weight (0 where not chosen)
+    T, H, I, E, k = (s[n] for n in ("T", "H", "I", "E", "k"))
+    x, idx = s["x"].float(), s["idx"].long()
+    scale = torch.zeros(T, E + 1, device=x.device).scatter_add(1, torch.where(idx < 0, E, idx), s["w"])[:, :E]
+    a = x @ s["w_gate"].float().view(E * I, H).t()
+    u = x @ s["w_up"].float().view(E * I, H).t()
+    h = (a / (1.0 + torch.exp(-a)) * u).view(T, E, I) * scale[:, :, None]
+    return (h.view(T, E * I) @ s["w_down"].float().transpose(1, 2).reshape(E * I, H)).to(torch.bfloat16)
+
+
+# ------------------------------------------------------------------ the framework's operators
+
+def _own_route(s):
+    from routed_grouped_gemm_softmax_b200 import api
+    return api.moe_route_scored(s["x"], s["k"], scoring=s["score"], bias=s["b"], n_groups=s["groups"],
+                                topk_groups=s["group_k"], group_score=s["group_score"], renormalize=s["renorm"],
+                                scale=s["scale"])
+
+
+def _own_linear(s):
+    from routed_grouped_gemm_softmax_b200 import api
+    return api.moe_linear(s["x"], s["w"], s["b"], act=s["act"], residual=s["r"], w_up=s["w_up"], bias_up=s["b_up"],
+                          out_dtype=torch.bfloat16 if s["out"] == "bf16" else torch.float32, ws=s["ws"])
+
+
+def _own_experts(s):
+    from routed_grouped_gemm_softmax_b200 import api
+    return api.moe_experts(s["x"], s["idx"], s["w"], s["w_gate"], s["w_up"], s["w_down"], ws=s["ws"])
+
+
+def run(state):
+    if own:
+        return {"route": _own_route, "linear": _own_linear, "experts": _own_experts}[state["op"]](state)
+    return {"route": _plain_route, "linear": _plain_linear, "experts": _plain_experts}[state["op"]](state)
+
+
+# ------------------------------------------------------------------ work
+
+def work(case):
+    if case["op"] == "route":
+        T, E, k = case["T"], case["E"], case["k"]
+        size = 4 if case["logits"] == "f32" else 2
+        # a score an expert (an exponential, counted as 10), a comparison a choice
+        return {"bytes": T * E * size + T * k * 8 + (4 * E if case["bias"] else 0), "flops": T * E * 12.0}
+    if case["op"] == "linear":
+        M, N, K = case["M"], case["N"], case["K"]
+        size, mats = (2 if case["out"] == "bf16" else 4), (2 if case["gated"] else 1)
+        vecs = mats if case["bias"] else 0
+        return {"bytes": 2 * M * K + 2 * N * K * mats + 4 * N * vecs + M * N * size * (2 if case["residual"] else 1),
+                "flops": 2.0 * M * N * K * mats}
+    T, H, I, E, k = (case[n] for n in ("T", "H", "I", "E", "k"))
+    rows = T - int(T * case["empty"])
+    touched = E * (1.0 - (1.0 - min(k, E) / E) ** rows)  # experts that a batch of `rows` tokens meets
+    return {"bytes": touched * 3 * I * H * 2 + 2 * T * H * 2 + T * k * 8, "flops": 6.0 * rows * k * I * H}
+
+
+# ------------------------------------------------------------------ 64 bits
+
+def _exact_route(s):
+    # choice by choice: the best remaining expert, the lowest index among equals
+    T, E, k, groups = s["T"], s["E"], s["k"], s["groups"]
+    z = s["x"].to(torch.float64)
+    bias = torch.zeros(E, dtype=torch.float64, device=z.device) if s["b"] is None else s["b"].to(torch.float64)
+    free = torch.isfinite(z) | (z == math.inf)
+    free &= torch.isfinite(bias) | (bias == math.inf)
+    z = torch.minimum(z, torch.tensor(F32_MAX, dtype=torch.float64, device=z.device))
+    z = z.masked_fill(~free, -math.inf)
+    if s["score"] == "sigmoid":
+        p = torch.sigmoid(z)
+    else:
+        p = torch.softmax(torch.where(free.any(1, keepdim=True), z, 0.0), dim=1).masked_fill(~free, 0.0)
+    key = z.clone() if s["b"] is None else (p + bias).masked_fill(~free, -math.inf)
+    lowest = torch.arange(E, device=z.device)
+
+    def take(c, n):
+        """The index of the largest of each row, the lowest of equal ones (n where none is left)."""
+        top = c.max(dim=1, keepdim=True).values
+        at = torch.where((c == top) & (c > -math.inf), torch.arange(c.shape[1], device=c.device), n)
+        return at.min(dim=1).values
+
+    if groups > 1:
+        each = E // groups
+        v = key if s["b"] is not None or s["group_score"] == "max" else p.masked_fill(~free, -math.inf)
+        v = v.view(T, groups, each)
+        first = v.max(dim=2)
+        score = first.values.clone()
+        if s["group_score"] == "top2" and each > 1:
+            rest = v.scatter(2, first.indices[:, :, None], -math.inf).max(dim=2).values
+            score = score + torch.where(rest == -math.inf, 0.0, rest)
+        allowed = torch.zeros(T, groups + 1, dtype=torch.bool, device=z.device)
+        for _ in range(s["group_k"]):
+            g = take(score, groups)
+            allowed[torch.arange(T, device=z.device), g] = True
+            score = torch.cat([score, score[:, :1]], 1).scatter(1, g[:, None], -math.inf)[:, :groups]
+        key = key.masked_fill(~allowed[:, lowest // each], -math.inf)
+    idx, w = [], []
+    for _ in range(k):
+        e = take(key, E)
+        idx.append(torch.where(e < E, e, -1))
+        w.append(torch.cat([p, torch.zeros_like(p[:, :1])], 1).gather(1, e[:, None])[:, 0])
+        key = torch.cat([key, key[:, :1]], 1).scatter(1, e[:, None], -math.inf)[:, :E]
+    idx, w = torch.stack(idx, 1), torch.stack(w, 1)
+    if s["renorm"]:
+        total = w.sum(1, keepdim=True)
+        w = torch.where(total > 0, w / total.clamp(min=1e-300), 0.0)
+    return idx.to(torch.int32), w * s["scale"]
+
+
+def _exact_linear(s):
+    M, N, K = s["M"], s["N"], s["K"]
+    if 2.0 * M * N * K * (2 if s["w_up"] is not None else 1) > 1e12:
+        return None
+    a = torch.nn.functional.linear(s["x"].double(), s["w"].double(), None if s["b"] is None else s["b"].double())
+    if s["act"] == "relu":
+        a = a.clamp(min=0)
+    elif s["act"] == "silu":
+        a = a * torch.sigmoid(a)
+    elif s["act"] == "gelu":
+        a = a * 0.5 * torch.special.erfc(-a / math.sqrt(2.0))
+    elif s["act"] == "gelu_tanh":
+        a = a * torch.sigmoid(2.0 * math.sqrt(2.0 / math.pi) * (a + 0.044715 * a ** 3))
+    if s["w_up"] is not None:
+        a = a * torch.nn.functional.linear(s["x"].double(), s["w_up"].double(),
+                                           None if s["b_up"] is None else s["b_up"].double())
+    return a if s["r"] is None else a + s["r"].double()
+
+
+def _exact_experts(s):
+    out = torch.zeros(s["T"], s["H"], dtype=torch.float64, device="cuda")
+    for e in range(s["E"]):
+        t, j = (s["idx"] == e).nonzero(as_tuple=True)
+        if not t.numel():
+            continue
+        x = s["x"][t].double()
+        a = x @ s["w_gate"][e].double().T
+        h = a * torch.sigmoid(a) * (x @ s["w_up"][e].double().T)
+        out.index_add_(0, t, (h @ s["w_down"][e].double().T) * s["w"][t, j].double()[:, None])
+    return out
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    return {"route": _exact_route, "linear": _exact_linear, "experts": _exact_experts}[case["op"]](s)
