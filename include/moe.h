@@ -108,6 +108,46 @@ moe_status_t moe_route(const moe_dims_t *d, const void *x, const void *router_w,
                        const float *router_bias, int32_t *topk_idx, float *topk_w,
                        void *ws, size_t ws_bytes, void *stream);
 
+/* Scored routing: the top-k experts of router logits that are given, in the forms that
+ * moe_route's softmax over the chosen logits does not cover.  For a row l of E logits
+ *   p[e] = 1 / (1 + exp(-l[e]))  (MOE_SCORE_SIGMOID), or the softmax of l over the
+ *          available experts     (MOE_SCORE_SOFTMAX)
+ *   c[e] = p[e] + bias[e], the value that decides the choice; without a bias the order
+ *          of p is that of l, and c[e] = l[e]
+ * With n_groups > 1 the experts are n_groups runs of E / n_groups; a group's value is
+ * the largest c of its experts (MOE_GROUP_MAX) or the sum of the two largest, taken of p
+ * without a bias (MOE_GROUP_TOP2; of one available expert, that one's), and only
+ * experts of the topk_groups groups of largest value can be chosen.  The top_k largest c are
+ * chosen in descending order; equal values go to the lower index, of experts and of
+ * groups.  With w[j] = p of choice j, renormalize divides w by its sum (0 for a sum of
+ * 0); then w is multiplied by `scale`.
+ * An expert is available to a row unless its logit or its bias is NaN or -inf; a +inf
+ * logit counts as the largest finite float.  Slots for which no available expert is
+ * left hold index -1 and weight 0 (all of them in a padded row of -inf): moe_experts
+ * skips them.  Choices are those of 64-bit scores, whatever the order of evaluation;
+ * weights are fp32.
+ *   logits [T, E] fp32 or bf16, rows `ld` >= E elements apart; bias [E] fp32, nullable
+ *   ->  topk_idx [T, top_k] int32, topk_w [T, top_k] fp32
+ * MOE_ERR_INVALID_ARG: as the rules above, E not a multiple of n_groups, topk_groups
+ * outside [1, n_groups], top_k above the experts of topk_groups groups, an unknown
+ * enum value, a pointer not aligned to its elements.  MOE_ERR_UNSUPPORTED: E > 1024,
+ * n_groups > 32.  Needs no workspace. */
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 };
+enum { MOE_LOGITS_F32 = 0, MOE_LOGITS_BF16 = 1 };
+typedef struct {
+    int32_t T, E, top_k;
+    int32_t scoring;               /* MOE_SCORE_* */
+    int32_t n_groups, topk_groups; /* 1, 1: no groups */
+    int32_t group_score;           /* MOE_GROUP_* */
+    int32_t renormalize;
+    float scale;
+    int32_t logits_dtype;          /* MOE_LOGITS_* */
+    int64_t ld;                    /* elements from one row of logits to the next */
+} moe_scored_t;
+moe_status_t moe_route_scored(const moe_scored_t *o, const void *logits, const float *bias,
+                              int32_t *topk_idx, float *topk_w, void *stream);
+
 /* Permute: group the flat assignments by expert (vLLM fused-MoE page, section
  * 02: tokens are sorted and grouped by expert before the grouped GEMM).  A
  * stable counting sort by expert of f = 0..T*k-1:

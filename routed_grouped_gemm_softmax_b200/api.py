@@ -26,7 +26,7 @@ EXPORTS = ["moe_workspace_size", "moe_max_tiles", "moe_route", "moe_permute", "m
            "moe_forward_fp8", "moe_quantize_rows_fp8", "moe_workspace_offsets", "moe_set_router_audit",
            "moe_forward_shared", "moe_workspace_size_shared", "moe_forward_mx", "moe_quantize_rows_mx",
            "moe_set_fused_combine", "moe_set_layer_gemm", "moe_forward_plan", "moe_set_direct_a",
-           "moe_set_cert_staging", "moe_noalloc_get_device_status"]
+           "moe_set_cert_staging", "moe_noalloc_get_device_status", "moe_route_scored"]
 DTYPE_BF16, DTYPE_FP8, DTYPE_MX = 0, 1, 2
 NOALLOC_SCRATCH_BYTES = 16 << 20
 STAGES = ["route", "permute", "gemm_gate_up", "gemm_down", "combine"]
@@ -42,6 +42,13 @@ class MoEError(RuntimeError):
 class Dims(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("I", ctypes.c_int32),
                 ("E", ctypes.c_int32), ("top_k", ctypes.c_int32)]
+
+
+class Scored(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("E", ctypes.c_int32), ("top_k", ctypes.c_int32), ("scoring", ctypes.c_int32),
+                ("n_groups", ctypes.c_int32), ("topk_groups", ctypes.c_int32), ("group_score", ctypes.c_int32),
+                ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float), ("logits_dtype", ctypes.c_int32),
+                ("ld", ctypes.c_int64)]
 
 
 _lib = None
@@ -112,6 +119,8 @@ def lib():
         L.moe_forward_noalloc.restype = ctypes.c_int
         L.moe_noalloc_get_device_status.argtypes = [P]
         L.moe_noalloc_get_device_status.restype = ctypes.c_int
+        L.moe_route_scored.argtypes = [ctypes.POINTER(Scored), P, P, P, P, P]
+        L.moe_route_scored.restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -135,6 +144,44 @@ def _need(t, dtype, shape, name):
     if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or not t.is_cuda:
         raise ValueError(f"{name}: expected contiguous CUDA {dtype} {tuple(shape)}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _need_on(t, dev, dtype, shape, name):
+    """A contiguous tensor of this type and shape on `dev` (the device of the call's first argument)."""
+    if t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on {dev}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _rows_of(t, dev, dtypes, shape, name) -> int:
+    """The row stride, in elements, of a matrix of this shape whose rows are contiguous."""
+    if t.dtype not in dtypes or t.shape != shape or t.device != dev or (t.stride(1) != 1 and shape[1] > 1):
+        raise ValueError(f"{name}: expected {' or '.join(map(str, dtypes))} {tuple(shape)} with contiguous rows on "
+                         f"{dev}, got {t.dtype} {tuple(t.shape)}, strides {t.stride()}, on {t.device}")
+    return t.stride(0) if shape[0] > 1 else max(t.stride(0), shape[1])
+
+
+def _empty(shape, dtype, dev, stream):
+    """A new tensor that belongs to the stream the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _call(fn, where, dev, stream, *args):
+    """fn(*args, stream) with `dev` current; `stream` (default: dev's current one) must be of `dev`."""
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device != dev:
+        raise ValueError(f"{where}: a stream of {stream.device} for tensors on {dev}")
+    if torch.cuda.current_device() == dev.index:
+        code = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args, stream.cuda_stream)
+    if code != MOE_OK:
+        raise MoEError(code, where)
 
 
 def dims(T, H, I, E, top_k) -> Dims:
@@ -172,6 +219,40 @@ def moe_route(x, router_w, bias, top_k: int, topk_idx=None, topk_w=None, ws=None
     d = dims(T, H, I, E, top_k)
     _check(lib().moe_route(ctypes.byref(d), _p(x), _p(router_w), _p(bias), _p(topk_idx), _p(topk_w),
                            _p(ws), ws.numel(), _stream(stream, dev)), "moe_route")
+    return topk_idx, topk_w
+
+
+SCORINGS = {"softmax": 0, "sigmoid": 1}
+GROUP_SCORES = {"max": 0, "top2": 1}
+
+
+def moe_route_scored(logits, top_k: int, scoring: str = "softmax", bias=None, n_groups: int = 1, topk_groups: int = 1,
+                     group_score: str = "max", renormalize: bool = True, scale: float = 1.0, topk_idx=None, topk_w=None,
+                     stream=None):
+    """Scored routing of router logits [T, E] (fp32 or bf16, contiguous rows): softmax or sigmoid
+    scores, an optional selection bias fp32 [E], group-limited top-k, weights renormalised and
+    scaled; returns (topk_idx int32 [T,k], -1 where no expert is available, topk_w fp32 [T,k])."""
+    if logits.dim() != 2 or not logits.is_cuda:
+        raise ValueError(f"logits: expected a CUDA matrix [T, E], got {tuple(logits.shape)} on {logits.device}")
+    T, E = logits.shape
+    dev = logits.device
+    ld = _rows_of(logits, dev, (torch.float32, torch.bfloat16), logits.shape, "logits")
+    if bias is not None:
+        _need_on(bias, dev, torch.float32, (E,), "bias")
+    if scoring not in SCORINGS or group_score not in GROUP_SCORES:
+        raise ValueError(f"scoring {scoring!r} (of {list(SCORINGS)}), group_score {group_score!r} (of {list(GROUP_SCORES)})")
+    if topk_idx is None:
+        topk_idx = _empty((T, top_k), torch.int32, dev, stream)
+    else:
+        _need_on(topk_idx, dev, torch.int32, (T, top_k), "topk_idx")
+    if topk_w is None:
+        topk_w = _empty((T, top_k), torch.float32, dev, stream)
+    else:
+        _need_on(topk_w, dev, torch.float32, (T, top_k), "topk_w")
+    o = Scored(T, E, top_k, SCORINGS[scoring], n_groups, topk_groups, GROUP_SCORES[group_score], bool(renormalize),
+               scale, logits.dtype == torch.bfloat16, ld)
+    _call(lib().moe_route_scored, "moe_route_scored", dev, stream, ctypes.byref(o), logits.data_ptr(),
+          None if bias is None else bias.data_ptr(), topk_idx.data_ptr(), topk_w.data_ptr())
     return topk_idx, topk_w
 
 

@@ -357,6 +357,23 @@ cudaError_t tc_router_logits(const __nv_bfloat16 *x, const __nv_bfloat16 *wrt, i
 // plus, with sh_count > 0, the shared expert's rows y[sh_rows0 + s * T + t] at gate 1.
 cudaError_t launch_combine(const __nv_bfloat16 *y, const float *gate, int T, int H, int top_k,
                            __nv_bfloat16 *out, cudaStream_t st, int sh_count = 0, int sh_rows0 = 0);
+// Scored routing of given logits (route_scored.cu): rows of E logits `ld` elements
+// apart, fp32 or (bf16 = true) bf16.
+struct ScoredArgs {
+    const void *logits;
+    int64_t ld;
+    const float *bias;  // or null
+    int T, E, k;
+    bool sigmoid;  // else softmax
+    int groups, topk_groups;
+    bool top2;  // a group's value: the sum of its two best, else its best
+    bool renormalize;
+    float scale;
+    int32_t *idx;
+    float *w;
+};
+cudaError_t launch_route_scored(const ScoredArgs &a, bool bf16, cudaStream_t st);
+
 // ----------------------------------------------------------- tile table
 // The kernel variants by M bucket: the batch's average rows per expert r = T*k/E (the
 // vLLM fused-MoE page keys its tuned configs by M the same way, section 03).  Measured
