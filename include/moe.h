@@ -192,6 +192,37 @@ moe_status_t moe_forward_shared(const moe_dims_t *d, const void *x, const void *
                                 const void *shared_up, const void *shared_down, void *out, void *ws,
                                 size_t ws_bytes, void *stream);
 
+/* Dense product with its elementwise work in the epilogue, for the layers around the
+ * routed one (projections, dense and shared FFN halves of any width, router logits):
+ *   out = act(x w^T + bias) [* (x w_up^T + bias_up)] [+ residual]
+ *   x [M, K] bf16, w [N, K] bf16 (K-major, nn.Linear style), w_up like w or NULL,
+ *   bias, bias_up [N] fp32 or NULL (bias_up only with w_up), residual [M, N] of the
+ *   output's type or NULL, out [M, N] bf16 or fp32.
+ * Rows are ldx, ldw (w and w_up), ldr, ldo elements apart.  gelu is the erf form v Phi(v),
+ * gelu_tanh its tanh approximation, silu v / (1 + exp(-v)).  Products are summed in
+ * fp32 on the tensor cores and everything after them in fp32; out is rounded once.  The order
+ * of every sum is fixed by the dims.  out may be residual itself (same rows); it may
+ * overlap nothing else that the call reads.
+ * The workspace holds moe_linear_workspace_size() bytes, 256-byte aligned, that are
+ * ZERO before its first call; calls leave it zero unless a pipeline wait ran out, which
+ * moe_get_device_status(ws, stream) reports and clears.
+ * MOE_ERR_INVALID_ARG: N or K <= 0, a row stride below the row's length, ldx or ldw not a
+ * multiple of 8 (the stride of a single row is not read), x, w or w_up not 16-byte
+ * aligned, bias_up without w_up, an unknown enum value, other pointers not aligned to
+ * their elements.  M == 0 is a no-op that returns MOE_OK. */
+enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_GELU = 2, MOE_ACT_GELU_TANH = 3, MOE_ACT_SILU = 4 };
+enum { MOE_OUT_BF16 = 0, MOE_OUT_F32 = 1 };
+typedef struct {
+    int32_t M, N, K;
+    int32_t act;        /* MOE_ACT_* */
+    int32_t out_dtype;  /* MOE_OUT_* */
+    int64_t ldx, ldw, ldr, ldo;
+} moe_linear_t;
+size_t moe_linear_workspace_size(void);
+moe_status_t moe_linear(const moe_linear_t *d, const void *x, const void *w, const void *w_up, const float *bias,
+                        const float *bias_up, const void *residual, void *out, void *ws, size_t ws_bytes,
+                        void *stream);
+
 /* FP8 block-scaled layer (GC-MoE page: block-scaled FP8 MMA on Blackwell with
  * SwiGLU and requantisation fused; vLLM fused-MoE page, section 03: fp8 weights
  * in [128,128] blocks).  Routing is the bf16 router of moe_route.  Weights are

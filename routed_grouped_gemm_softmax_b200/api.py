@@ -26,7 +26,8 @@ EXPORTS = ["moe_workspace_size", "moe_max_tiles", "moe_route", "moe_permute", "m
            "moe_forward_fp8", "moe_quantize_rows_fp8", "moe_workspace_offsets", "moe_set_router_audit",
            "moe_forward_shared", "moe_workspace_size_shared", "moe_forward_mx", "moe_quantize_rows_mx",
            "moe_set_fused_combine", "moe_set_layer_gemm", "moe_forward_plan", "moe_set_direct_a",
-           "moe_set_cert_staging", "moe_noalloc_get_device_status", "moe_route_scored"]
+           "moe_set_cert_staging", "moe_noalloc_get_device_status", "moe_route_scored", "moe_linear",
+           "moe_linear_workspace_size"]
 DTYPE_BF16, DTYPE_FP8, DTYPE_MX = 0, 1, 2
 NOALLOC_SCRATCH_BYTES = 16 << 20
 STAGES = ["route", "permute", "gemm_gate_up", "gemm_down", "combine"]
@@ -49,6 +50,12 @@ class Scored(ctypes.Structure):
                 ("n_groups", ctypes.c_int32), ("topk_groups", ctypes.c_int32), ("group_score", ctypes.c_int32),
                 ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float), ("logits_dtype", ctypes.c_int32),
                 ("ld", ctypes.c_int64)]
+
+
+class Linear(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("ldx", ctypes.c_int64), ("ldw", ctypes.c_int64),
+                ("ldr", ctypes.c_int64), ("ldo", ctypes.c_int64)]
 
 
 _lib = None
@@ -121,6 +128,10 @@ def lib():
         L.moe_noalloc_get_device_status.restype = ctypes.c_int
         L.moe_route_scored.argtypes = [ctypes.POINTER(Scored), P, P, P, P, P]
         L.moe_route_scored.restype = ctypes.c_int
+        L.moe_linear_workspace_size.argtypes = []
+        L.moe_linear_workspace_size.restype = SZ
+        L.moe_linear.argtypes = [ctypes.POINTER(Linear), P, P, P, P, P, P, P, P, SZ, P]
+        L.moe_linear.restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -333,6 +344,54 @@ def moe_forward_shared(x, router_w, bias, w_gate, w_up, w_down, shared_gate, sha
                                     _p(w_down), int(SI), _p(shared_gate), _p(shared_up), _p(shared_down), _p(out),
                                     _p(ws), ws.numel(), _stream(stream, dev)),
            "moe_forward_shared")
+    return out
+
+
+ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+_BF16 = (torch.bfloat16,)
+
+
+def linear_workspace(device, stream=None) -> torch.Tensor:
+    """A zeroed workspace for moe_linear, to be kept for later calls on one stream."""
+    with torch.cuda.stream(stream):
+        return torch.zeros(int(lib().moe_linear_workspace_size()), dtype=torch.uint8, device=device)
+
+
+def moe_linear(x, w, bias=None, act: str = "none", residual=None, w_up=None, bias_up=None, out=None,
+               out_dtype=torch.bfloat16, ws=None, stream=None):
+    """act(x w^T + bias) [* (x w_up^T + bias_up)] [+ residual]: x bf16 [M,K], w and w_up bf16
+    [N,K], biases fp32 [N], residual and out [M,N] of out_dtype (bf16 or fp32); rows contiguous,
+    those of x and w a multiple of 8 elements apart.  act: one of ACTS.  Returns out, which
+    may be residual."""
+    if x.dim() != 2 or w.dim() != 2 or not x.is_cuda:
+        raise ValueError(f"x, w: expected CUDA matrices [M, K] and [N, K], got {tuple(x.shape)} on {x.device} and "
+                         f"{tuple(w.shape)}")
+    M, K = x.shape
+    N = w.shape[0]
+    dev = x.device
+    ldx = _rows_of(x, dev, _BF16, (M, K), "x")
+    ldw = _rows_of(w, dev, _BF16, (N, K), "w")
+    if w_up is not None and _rows_of(w_up, dev, _BF16, (N, K), "w_up") != ldw:
+        raise ValueError("w_up: its rows must be as far apart as those of w")
+    if bias is not None:
+        _need_on(bias, dev, torch.float32, (N,), "bias")
+    if bias_up is not None:
+        _need_on(bias_up, dev, torch.float32, (N,), "bias_up")
+    if act not in ACTS or out_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"act {act!r} (of {list(ACTS)}), out_dtype {out_dtype} (bf16 or fp32)")
+    ldr = 0 if residual is None else _rows_of(residual, dev, (out_dtype,), (M, N), "residual")
+    if out is None:
+        out = _empty((M, N), out_dtype, dev, stream)
+    ldo = _rows_of(out, dev, (out_dtype,), (M, N), "out")
+    if ws is None:
+        ws = linear_workspace(dev, stream)
+    elif ws.device != dev:
+        raise ValueError(f"ws: on {ws.device}, expected {dev}")
+    d = Linear(M, N, K, ACTS[act], out_dtype == torch.float32, ldx, ldw, ldr, ldo)
+    _call(lib().moe_linear, "moe_linear", dev, stream, ctypes.byref(d), x.data_ptr(), w.data_ptr(),
+          None if w_up is None else w_up.data_ptr(), None if bias is None else bias.data_ptr(),
+          None if bias_up is None else bias_up.data_ptr(), None if residual is None else residual.data_ptr(),
+          out.data_ptr(), ws.data_ptr(), ws.numel())
     return out
 
 

@@ -313,6 +313,32 @@ bool encode_plain_2d_bf16(CUtensorMap *m, const void *base, uint64_t rows, uint6
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_sw128_bf16(CUtensorMap *m, const void *base, uint32_t rank, const uint64_t *dims, const uint64_t *strides,
+                       const uint32_t *box)
+{
+    EncodeTiledFn f = encode_fn();
+    if (!f || rank < 2 || rank > 5) return false;
+    static_assert(sizeof(cuuint64_t) == sizeof(uint64_t) && sizeof(cuuint32_t) == sizeof(uint32_t), "map types");
+    const cuuint32_t es[5] = {1, 1, 1, 1, 1};
+    cuuint64_t dm[5], sd[4];
+    cuuint32_t bx[5];
+    for (uint32_t i = 0; i < rank; ++i) {
+        dm[i] = dims[i];
+        bx[i] = box[i];
+        if (i + 1 < rank) sd[i] = strides[i];
+    }
+    return f(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dm, sd, bx, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+void wait_settings(uint64_t *wait_ns, int *stall_test)
+{
+    const unsigned long long wl = g_wait_ns.load();
+    *wait_ns = wl ? wl : 2000000000ull;
+    *stall_test = g_stall_test.load();
+}
+
 // bf16 matrix [rows, cols], tiles of box_rows x 64 with the 128-byte swizzle.
 bool encode_sw128_2d_bf16(CUtensorMap *m, const void *base, uint64_t rows, uint64_t cols, uint32_t box_rows)
 {

@@ -416,6 +416,14 @@ constexpr int kFusedCombineMaxTFp8 = 64;
 
 int num_sms();
 
+// The limit of each pipeline wait and the stall test, as moe_set_wait_limit_us left them.
+void wait_settings(uint64_t *wait_ns, int *stall_test);
+
+// Tensor map of bf16 elements with the 128-byte swizzle: dims and box innermost first,
+// strides (bytes) of the dims after the first; elements outside read as zero.
+bool encode_sw128_bf16(CUtensorMap *m, const void *base, uint32_t rank, const uint64_t *dims, const uint64_t *strides,
+                       const uint32_t *box);
+
 // Tensor map of a row-major bf16 matrix [rows, cols], box_rows x 64 tiles with the
 // 128-byte swizzle (16-byte chunk c of tile row r stored at chunk c ^ (r % 8)).
 bool encode_sw128_2d_bf16(CUtensorMap *m, const void *base, uint64_t rows, uint64_t cols, uint32_t box_rows);
