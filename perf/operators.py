@@ -158,7 +158,7 @@ def prepare(case, seed):
             s["w"][T - n:] = 0.0
         if own:
             from routed_grouped_gemm_softmax_b200 import api
-            s["ws"] = api.workspace(T, H, I, E, k, "cuda")
+            s["ws"] = api.experts_workspace(T, H, I, E, k, "cuda")
     return s
 
 
