@@ -172,6 +172,29 @@ moe_status_t moe_forward(const moe_dims_t *d, const void *x, const void *router_
                          const float *router_bias, const void *w_gate, const void *w_up,
                          const void *w_down, void *out, void *ws, size_t ws_bytes, void *stream);
 
+/* The experts' products on a routing that is given, for routers other than moe_route's
+ * softmax (moe_route_scored, or the caller's own):
+ *   out[t] = sum_j topk_w[t,j] * FFN_{topk_idx[t,j]}(x_t)
+ * A slot with index -1 has no expert and adds nothing, whatever its weight; a token whose
+ * slots are all -1 gets zeros.  Other indices outside [0,E) are skipped the same way
+ * and flagged MOE_ERR_BAD_INDEX.  An expert may come twice in a token.  The kernels and
+ * roundings are moe_forward's (moe_forward_fp8's, moe_forward_mx's) but for the bf16
+ * form's per-assignment expert outputs, which stay in fp32 until the weighted sum.
+ * ws_bytes >= moe_experts_workspace_size(d, dtype), the dtype that of the weights; other
+ * rules as the forward of that dtype. */
+size_t moe_experts_workspace_size(const moe_dims_t *d, int dtype);
+moe_status_t moe_experts(const moe_dims_t *d, const void *x, const int32_t *topk_idx, const float *topk_w,
+                         const void *w_gate, const void *w_up, const void *w_down, void *out, void *ws,
+                         size_t ws_bytes, void *stream);
+moe_status_t moe_experts_fp8(const moe_dims_t *d, const void *x, const int32_t *topk_idx, const float *topk_w,
+                             const uint8_t *w_gate_q, const float *w_gate_s, const uint8_t *w_up_q,
+                             const float *w_up_s, const uint8_t *w_down_q, const float *w_down_s, void *out, void *ws,
+                             size_t ws_bytes, void *stream);
+moe_status_t moe_experts_mx(const moe_dims_t *d, const void *x, const int32_t *topk_idx, const float *topk_w,
+                            const uint8_t *w_gate_p, const uint8_t *w_gate_x, const uint8_t *w_up_p,
+                            const uint8_t *w_up_x, const uint8_t *w_down_p, const uint8_t *w_down_x, void *out,
+                            void *ws, size_t ws_bytes, void *stream);
+
 /* The layer with a shared expert (GC-MoE page, compute-partition section: the
  * block-scaled expert kernel with "optional shared experts" fused in).  Besides the
  * k routed experts, every token passes through one shared SwiGLU expert with gate

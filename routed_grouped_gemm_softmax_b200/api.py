@@ -27,7 +27,7 @@ EXPORTS = ["moe_workspace_size", "moe_max_tiles", "moe_route", "moe_permute", "m
            "moe_forward_shared", "moe_workspace_size_shared", "moe_forward_mx", "moe_quantize_rows_mx",
            "moe_set_fused_combine", "moe_set_layer_gemm", "moe_forward_plan", "moe_set_direct_a",
            "moe_set_cert_staging", "moe_noalloc_get_device_status", "moe_route_scored", "moe_linear",
-           "moe_linear_workspace_size"]
+           "moe_linear_workspace_size", "moe_experts", "moe_experts_fp8", "moe_experts_mx", "moe_experts_workspace_size"]
 DTYPE_BF16, DTYPE_FP8, DTYPE_MX = 0, 1, 2
 NOALLOC_SCRATCH_BYTES = 16 << 20
 STAGES = ["route", "permute", "gemm_gate_up", "gemm_down", "combine"]
@@ -128,6 +128,14 @@ def lib():
         L.moe_noalloc_get_device_status.restype = ctypes.c_int
         L.moe_route_scored.argtypes = [ctypes.POINTER(Scored), P, P, P, P, P]
         L.moe_route_scored.restype = ctypes.c_int
+        L.moe_experts_workspace_size.argtypes = [D, ctypes.c_int]
+        L.moe_experts_workspace_size.restype = SZ
+        L.moe_experts.argtypes = [D, P, P, P, P, P, P, P, P, SZ, P]
+        L.moe_experts.restype = ctypes.c_int
+        L.moe_experts_fp8.argtypes = [D, P, P, P, P, P, P, P, P, P, P, P, SZ, P]
+        L.moe_experts_fp8.restype = ctypes.c_int
+        L.moe_experts_mx.argtypes = [D, P, P, P, P, P, P, P, P, P, P, P, SZ, P]
+        L.moe_experts_mx.restype = ctypes.c_int
         L.moe_linear_workspace_size.argtypes = []
         L.moe_linear_workspace_size.restype = SZ
         L.moe_linear.argtypes = [ctypes.POINTER(Linear), P, P, P, P, P, P, P, P, SZ, P]
@@ -308,6 +316,80 @@ def moe_forward(x, router_w, bias, w_gate, w_up, w_down, top_k: int, out=None, w
                              _p(w_down), _p(out), _p(ws), ws.numel(), _stream(stream, dev)),
            "moe_forward")
     return out
+
+
+def experts_workspace(T, H, I, E, top_k, device, dtype: int = DTYPE_BF16, stream=None) -> torch.Tensor:
+    """A workspace for moe_experts (moe_experts_fp8, moe_experts_mx: their dtype), reusable across
+    calls on one stream."""
+    n = int(lib().moe_experts_workspace_size(ctypes.byref(dims(T, H, I, E, top_k)), int(dtype)))
+    if n == 0:
+        raise MoEError(1, "moe_experts_workspace_size")
+    return _empty(n, torch.uint8, device, stream)
+
+
+def _experts(fn, where, dtype, x, topk_idx, topk_w, E, I, weights, out, ws, stream):
+    """The part that the three weight types share; `weights` as (tensor, dtype, shape, name)."""
+    T, H = x.shape
+    dev = x.device
+    k = topk_idx.shape[-1]
+    _need_on(x, dev, torch.bfloat16, (T, H), "x")
+    _need_on(topk_idx, dev, torch.int32, (T, k), "topk_idx")
+    _need_on(topk_w, dev, torch.float32, (T, k), "topk_w")
+    for t, dt, shape, name in weights:
+        _need_on(t, dev, dt, shape, name)
+    if out is None:
+        out = _empty((T, H), torch.bfloat16, dev, stream)
+    else:
+        _need_on(out, dev, torch.bfloat16, (T, H), "out")
+    if ws is None:
+        ws = experts_workspace(T, H, I, E, k, dev, dtype, stream)
+    elif ws.device != dev:
+        raise ValueError(f"ws: on {ws.device}, expected {dev}")
+    d = dims(T, H, I, E, k)
+    _call(fn, where, dev, stream, ctypes.byref(d), x.data_ptr(), topk_idx.data_ptr(), topk_w.data_ptr(),
+          *[t.data_ptr() for t, _, _, _ in weights], out.data_ptr(), ws.data_ptr(), ws.numel())
+    return out
+
+
+def _experts_shape(x, w_gate):
+    if x.dim() != 2 or w_gate.dim() != 3 or not x.is_cuda:
+        raise ValueError(f"x, gate weights: expected CUDA tensors [T, H] and [E, I, .], got {tuple(x.shape)} on "
+                         f"{x.device} and {tuple(w_gate.shape)}")
+    return x.shape[1], w_gate.shape[0], w_gate.shape[1]
+
+
+def moe_experts(x, topk_idx, topk_w, w_gate, w_up, w_down, out=None, ws=None, stream=None):
+    """The experts' products on a given routing: topk_idx int32 [T,k] (-1: no expert), topk_w
+    fp32 [T,k]; weights as moe_forward's; ws from experts_workspace; returns out bf16 [T,H]."""
+    H, E, I = _experts_shape(x, w_gate)
+    b = torch.bfloat16
+    return _experts(lib().moe_experts, "moe_experts", DTYPE_BF16, x, topk_idx, topk_w, E, I,
+                    ((w_gate, b, (E, I, H), "w_gate"), (w_up, b, (E, I, H), "w_up"), (w_down, b, (E, H, I), "w_down")),
+                    out, ws, stream)
+
+
+def moe_experts_fp8(x, topk_idx, topk_w, w_gate_q, w_gate_s, w_up_q, w_up_s, w_down_q, w_down_s, out=None, ws=None,
+                    stream=None):
+    """moe_experts with moe_forward_fp8's weights."""
+    H, E, I = _experts_shape(x, w_gate_q)
+    u, f = torch.uint8, torch.float32
+    return _experts(lib().moe_experts_fp8, "moe_experts_fp8", DTYPE_FP8, x, topk_idx, topk_w, E, I,
+                    ((w_gate_q, u, (E, I, H), "w_gate_q"), (w_gate_s, f, (E, I // 128, H // 128), "w_gate_s"),
+                     (w_up_q, u, (E, I, H), "w_up_q"), (w_up_s, f, (E, I // 128, H // 128), "w_up_s"),
+                     (w_down_q, u, (E, H, I), "w_down_q"), (w_down_s, f, (E, H // 128, I // 128), "w_down_s")),
+                    out, ws, stream)
+
+
+def moe_experts_mx(x, topk_idx, topk_w, w_gate_p, w_gate_x, w_up_p, w_up_x, w_down_p, w_down_x, out=None, ws=None,
+                   stream=None):
+    """moe_experts with moe_forward_mx's weights."""
+    H, E, I = _experts_shape(x, w_gate_p)
+    u = torch.uint8
+    return _experts(lib().moe_experts_mx, "moe_experts_mx", DTYPE_MX, x, topk_idx, topk_w, E, I,
+                    ((w_gate_p, u, (E, I, H // 2), "w_gate_p"), (w_gate_x, u, (E, I, H // 32), "w_gate_x"),
+                     (w_up_p, u, (E, I, H // 2), "w_up_p"), (w_up_x, u, (E, I, H // 32), "w_up_x"),
+                     (w_down_p, u, (E, H, I // 2), "w_down_p"), (w_down_x, u, (E, H, I // 32), "w_down_x")),
+                    out, ws, stream)
 
 
 def moe_workspace_size_shared(T, H, I, E, top_k, shared_I) -> int:

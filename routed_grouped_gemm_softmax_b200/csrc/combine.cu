@@ -20,7 +20,61 @@ __global__ void __launch_bounds__(256) combine_kernel(const __nv_bfloat16 *__res
         combine_cols<false>(y, gate, out, t, k, H, c0 + threadIdx.x * 8, sh_count, T, sh_rows0);
 }
 
+__device__ __forceinline__ void load8(const float *p, float (&v)[8])
+{
+    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&v)[8])
+{
+    const uint4 a = *reinterpret_cast<const uint4 *>(p);
+    const __nv_bfloat162 *q = reinterpret_cast<const __nv_bfloat162 *>(&a);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __bfloat1622float2(q[i]);
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+    }
+}
+
+// out[t] = bf16(sum of w[t,j] y[t*k + j] over the slots j with an expert), fp32 fma in
+// ascending j.  A slot without an expert has no y row: its memory is not read.
+template <typename TY>
+__global__ void __launch_bounds__(256) combine_given_kernel(const TY *__restrict__ y, const int32_t *__restrict__ idx,
+                                                            const float *__restrict__ w, int H, int E, int k,
+                                                            __nv_bfloat16 *__restrict__ out)
+{
+    pdl_wait();
+    pdl_trigger();
+    const size_t t = blockIdx.x;
+    for (int c = threadIdx.x * 8; c < H; c += 256 * 8) {
+        float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < k; ++j) {
+            if ((unsigned)idx[t * k + j] >= (unsigned)E) continue;
+            const float g = w[t * k + j];
+            float v[8];
+            load8(y + (t * k + j) * H + c, v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[i] = fmaf(g, v[i], acc[i]);
+        }
+        uint4 o;
+        __nv_bfloat162 *q = reinterpret_cast<__nv_bfloat162 *>(&o);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q[i] = __floats2bfloat162_rn(acc[2 * i], acc[2 * i + 1]);
+        *reinterpret_cast<uint4 *>(out + t * H + c) = o;
+    }
+}
+
 }  // namespace
+
+cudaError_t launch_combine_given(const void *y, bool y_f32, const int32_t *idx, const float *w, int T, int H, int E,
+                                 int top_k, __nv_bfloat16 *out, cudaStream_t st)
+{
+    return y_f32 ? launch_pdl(combine_given_kernel<float>, dim3(T), dim3(256), 0, st, static_cast<const float *>(y),
+                              idx, w, H, E, top_k, out)
+                 : launch_pdl(combine_given_kernel<__nv_bfloat16>, dim3(T), dim3(256), 0, st,
+                              static_cast<const __nv_bfloat16 *>(y), idx, w, H, E, top_k, out);
+}
 
 cudaError_t launch_combine(const __nv_bfloat16 *y, const float *gate, int T, int H, int top_k,
                            __nv_bfloat16 *out, cudaStream_t st, int sh_count, int sh_rows0)

@@ -492,7 +492,13 @@ grouped_gemm_kernel(const __grid_constant__ AMaps tmA, const __grid_constant__ C
                     uint32_t r[32];
                     tmem_ld32_sync(tb + c * 32, r);
                     const int col = nt * BNO1 + c * 32;
-                    if (row_ok && col < N) {
+                    if (row_ok && col < N && g.y_f32) {
+                        float4 *dst = reinterpret_cast<float4 *>(g.y_f32 + (size_t)flat * N + col);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            dst[i] = make_float4(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]),
+                                                 __uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3]));
+                    } else if (row_ok && col < N) {
                         uint32_t pk[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) pk[i] = pack_bf16(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));

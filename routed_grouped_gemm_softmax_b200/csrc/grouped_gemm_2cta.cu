@@ -534,7 +534,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS2, 1)
                     uint32_t r[32];
                     tmem_ld32_sync(tb + c * 32, r);
                     const int col = nt * BNO1 + c * 32;
-                    if (row_ok && col < NP1) {
+                    if (row_ok && col < NP1 && g.y_f32) {
+                        float4 *dst = reinterpret_cast<float4 *>(g.y_f32 + (size_t)flat * NP1 + col);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            dst[i] = make_float4(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]),
+                                                 __uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3]));
+                    } else if (row_ok && col < NP1) {
                         uint32_t pk[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i)

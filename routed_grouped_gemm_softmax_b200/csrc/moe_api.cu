@@ -244,14 +244,16 @@ moe::RouterScratch router_scratch(void *ws, const moe::WsLayout &L, const moe_di
 
 // The bf16 forward's choice of kernels for these dims under the current settings
 // (MOE_PLAN_* bits).
-int bf16_plan(const moe_dims_t &d)
+// On a given routing there is no router and no fused combine, whose arrival counts
+// take every slot to have an expert.
+int bf16_plan(const moe_dims_t &d, bool given = false)
 {
     const moe::TileChoice tc = moe::tile_choice((long long)d.T * d.top_k, d.E);
-    const bool small = moe::small_route_permute_ok(d);
+    const bool small = !given && moe::small_route_permute_ok(d);
     const int pair_mode = g_pair_mode.load();
     const bool pairs = pair_mode != 2 && g_claim_reverse.load() <= 1 && !small && (pair_mode == 1 || tc.pair_tiles);
     const int fc = g_fused_comb.load();
-    const bool fused = fc == 1 || (fc == 0 && d.T <= moe::kFusedCombineMaxT);
+    const bool fused = !given && (fc == 1 || (fc == 0 && d.T <= moe::kFusedCombineMaxT));
     const int lg = g_layer_gemm.load();
     const bool layer = lg == 1 || (lg == 0 && tc.layer_gemm);
     const int da = g_direct_a.load();
@@ -263,6 +265,16 @@ int bf16_plan(const moe_dims_t &d)
 // Activations, weights and outputs are read and written in 16-byte vectors (and the
 // weights by TMA, which needs 16-byte aligned bases).
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// A routing that the caller gives: [T, k] expert indices (-1: no expert) and weights.
+struct GivenRouting {
+    const int32_t *idx;
+    const float *w;
+    bool ok() const
+    {
+        return idx && w && reinterpret_cast<uintptr_t>(idx) % 4 == 0 && reinterpret_cast<uintptr_t>(w) % 4 == 0;
+    }
+};
 
 // Router and permute: one fused launch for small batches, otherwise the logits,
 // top-k and three permute kernels.  Stage mark 1 (routed) is recorded between the
@@ -406,6 +418,348 @@ cudaError_t tc_router_logits(const __nv_bfloat16 *x, const __nv_bfloat16 *wrt, i
 }
 }  // namespace moe
 
+namespace {
+
+// Clears the header and the counts behind it, then groups the assignments by expert:
+// the router's or, with `given`, the caller's.
+cudaError_t group_assignments(const moe_dims_t &d, const moe::WsLayout &L, const void *x, const void *router_w,
+                              const float *router_bias, const GivenRouting *given, void *ws, moe::WsHeader *hdr,
+                              const StageMarks &marks, cudaStream_t st)
+{
+    cudaError_t e = cudaSuccess;
+    if (given || !moe::small_route_permute_ok(d))  // else the router's kernels clear them
+        e = cudaMemsetAsync(hdr, 0, L.clear_bytes, st);
+    if (e != cudaSuccess) return e;
+    if (!given) return route_and_permute(d, L, x, router_w, router_bias, ws, hdr, marks, st);
+    e = marks.mark(1, st);
+    if (e == cudaSuccess)
+        e = moe::launch_permute(d, L, given->idx, at<int32_t>(ws, L.blk_cnt), at<int32_t>(ws, L.blk_base),
+                                at<int32_t>(ws, L.offsets), at<int32_t>(ws, L.s2f), at<int32_t>(ws, L.f2s),
+                                at<int32_t>(ws, L.tiles), at<int32_t>(ws, L.ntiles), hdr, st, at<int32_t>(ws, L.tiles2),
+                                at<int32_t>(ws, L.ntiles2), true);
+    return e;
+}
+
+// The bf16 layer.  `given` null: routed by x and router_w; else on that routing, router_w
+// and router_bias unused.
+moe_status_t forward_bf16(const moe_dims_t *d, const void *x, const void *router_w, const float *router_bias,
+                          const GivenRouting *given, const void *w_gate, const void *w_up, const void *w_down,
+                          int32_t shared_I, const void *shared_gate, const void *shared_up, const void *shared_down,
+                          void *out, void *ws, size_t ws_bytes, void *stream)
+{
+    moe_status_t s = check_dims(d);
+    if (s != MOE_OK) return s;
+    if (shared_I < 0 || shared_I % d->I != 0) return MOE_ERR_INVALID_ARG;
+    const int sh = shared_I / d->I;  // slices of the shared expert, I columns each
+    if (d->T == 0) return MOE_OK;
+    if (!x || !w_gate || !w_up || !w_down || !out) return MOE_ERR_INVALID_ARG;
+    if (given ? !given->ok() : !router_w || !aligned16(router_w)) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(w_gate) || !aligned16(w_up) || !aligned16(w_down) ||
+        !aligned16(out))
+        return MOE_ERR_INVALID_ARG;
+    if (sh && (!shared_gate || !shared_up || !shared_down || !aligned16(shared_gate) || !aligned16(shared_up) ||
+               !aligned16(shared_down)))
+        return MOE_ERR_INVALID_ARG;
+    if ((int64_t)sh * d->T + (int64_t)d->T * d->top_k > (int64_t)INT32_MAX / 2) return MOE_ERR_UNSUPPORTED;
+    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return MOE_ERR_WORKSPACE;
+    const moe::WsLayout L = moe::ws_layout(*d, MOE_DTYPE_BF16, sh, given != nullptr);
+    if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int A = d->T * d->top_k;
+    const int R = A + sh * d->T;  // rows of h and y: the routed assignments, then the shared expert's
+    auto *hdr = at<moe::WsHeader>(ws, 0);
+    auto *xs = at<__nv_bfloat16>(ws, L.xs);
+    auto *h = at<__nv_bfloat16>(ws, L.h);
+    auto *y = at<__nv_bfloat16>(ws, L.y);
+    auto *gate = at<float>(ws, L.gate);
+    auto *s2f = at<int32_t>(ws, L.s2f);
+    auto *tiles = at<int32_t>(ws, L.tiles);
+    auto *ntiles = at<int32_t>(ws, L.ntiles);
+
+    moe::AMaps tm_xs, tm_h;
+    CUtensorMap tm_wg, tm_wu, tm_wd;
+    // pair-of-CTA GEMMs for groups large enough to be compute-bound (on average at
+    // least 768 rows per expert), on the queue's claim modes
+    const int plan = bf16_plan(*d, given != nullptr);
+    const bool pairs = plan & MOE_PLAN_PAIR_TILES;
+    if (!moe::encode_a_maps(&tm_xs, xs, A, d->H, false) ||
+        !encode_4d_chunked(&tm_wg, w_gate, d->E, d->I, d->H, 128, 2) ||
+        !encode_4d_chunked(&tm_wu, w_up, d->E, d->I, d->H, 128, 2) ||
+        !moe::encode_a_maps(&tm_h, h, R, d->I, false) ||
+        !encode_4d_chunked(&tm_wd, w_down, d->E, d->H, d->I, pairs ? 128 : 256, 2))
+        return MOE_ERR_CUDA;
+    // the shared expert: x itself as its gate/up A operand, its weights as chunked maps
+    // with the boxes of the routed experts' maps
+    moe::SharedMaps sm1{}, sm2{};
+    if (sh && (!moe::encode_a_maps(&sm1.x, x, d->T, d->H, false) ||
+               !moe::encode_sw128_chunked_bf16(&sm1.b0, shared_gate, shared_I, d->H, 128, 2) ||
+               !moe::encode_sw128_chunked_bf16(&sm1.b1, shared_up, shared_I, d->H, 128, 2) ||
+               !moe::encode_sw128_chunked_bf16(&sm2.b0, shared_down, d->H, shared_I, pairs ? 128 : 256, 2)))
+        return MOE_ERR_CUDA;
+    // gate/up A rows straight from x: one-row boxes for tile::gather4, the token of
+    // sorted row r being sorted_to_flat[r] / k
+    const bool direct = plan & MOE_PLAN_DIRECT_A;
+    if (direct && !encode_2d(&sm1.xg, x, d->T, d->H, 1)) return MOE_ERR_CUDA;
+    // the tile list is then the output of the kernel just before the gate/up GEMM
+    // when the router and the grouping are one launch
+    const int tiles_first = direct && (plan & MOE_PLAN_SMALL_ROUTER) ? 1 : 0;
+
+    const StageMarks marks;
+    const bool fused = plan & MOE_PLAN_FUSED_COMBINE;  // combine inside the down GEMM
+    cudaError_t e = marks.mark(0, st);
+    if (e == cudaSuccess) e = group_assignments(*d, L, x, router_w, router_bias, given, ws, hdr, marks, st);
+    if (e == cudaSuccess && !direct)
+        e = moe::launch_gather_rows(static_cast<const __nv_bfloat16 *>(x), at<int32_t>(ws, L.f2s), d->T, d->H,
+                                    d->top_k, xs, st);
+    if (e == cudaSuccess) e = marks.mark(2, st);
+    const int ctas = g_gemm_ctas.load(), rev = g_claim_reverse.load();
+    unsigned long long *trace1 = g_trace.load(), *trace2 = trace1 ? trace1 + 2 * g_trace_ctas.load() : nullptr;
+    const unsigned long long wl = g_wait_ns.load();
+    const uint64_t wait_ns = wl ? wl : 2000000000ull;
+    const int stall = g_stall_test.load();
+    // the gate/up and the down GEMM in one persistent launch (readiness counters per
+    // m-tile hand h from one to the other)
+    const bool layer = plan & MOE_PLAN_LAYER_GEMM;
+    if (e == cudaSuccess && layer) {
+        moe::GemmArgs gl{3, d->H, d->I, tiles, ntiles, &hdr->counter[0], &hdr->status, h, s2f, ctas, rev, wait_ns,
+                         stall, 0, nullptr, gate, fused ? at<int32_t>(ws, L.ccnt) : nullptr,
+                         static_cast<__nv_bfloat16 *>(out), d->top_k, d->top_k + sh};
+        gl.trace = trace1;
+        gl.sh_count = sh;
+        gl.sh_T = d->T;
+        gl.sh_rows0 = A;
+        gl.sh_e0 = d->E;
+        gl.K2 = d->I;
+        gl.N2 = d->H;
+        gl.out2 = y;
+        gl.ready = at<int32_t>(ws, L.ready);
+        gl.y_f32 = given ? at<float>(ws, L.y) : nullptr;
+        if (direct) {
+            gl.a_rows = s2f;
+            gl.a_div = d->top_k;
+            gl.a_tokens = d->T;
+            gl.tiles_first = tiles_first;
+        }
+        moe::LayerMaps lm{};
+        lm.h = tm_h;
+        lm.wd = tm_wd;
+        lm.wd_sh = sm2.b0;
+        e = pairs ? moe::launch_grouped_gemm_2cta(gl, tm_xs, tm_wg, tm_wu, at<int32_t>(ws, L.tiles2),
+                                                  at<int32_t>(ws, L.ntiles2), st, &sm1, &lm)
+                  : moe::launch_grouped_gemm(gl, tm_xs, tm_wg, tm_wu, st, &sm1, &lm);
+        if (e == cudaSuccess) e = marks.mark(3, st);
+        if (e == cudaSuccess) e = marks.mark(4, st);
+    }
+    if (e == cudaSuccess && !layer) {
+        moe::GemmArgs g1{0, d->H, d->I, tiles, ntiles, &hdr->counter[0], &hdr->status, h, nullptr, ctas, rev, wait_ns, stall};
+        g1.trace = trace1;
+        g1.sh_count = sh;
+        g1.sh_T = d->T;
+        g1.sh_rows0 = A;
+        g1.sh_e0 = d->E;
+        if (direct) {
+            g1.a_rows = s2f;
+            g1.a_div = d->top_k;
+            g1.a_tokens = d->T;
+            g1.tiles_first = tiles_first;
+        }
+        e = pairs ? moe::launch_grouped_gemm_2cta(g1, tm_xs, tm_wg, tm_wu, at<int32_t>(ws, L.tiles2),
+                                                  at<int32_t>(ws, L.ntiles2), st, &sm1)
+                  : moe::launch_grouped_gemm(g1, tm_xs, tm_wg, tm_wu, st, &sm1);
+        if (e == cudaSuccess) e = marks.mark(3, st);
+    }
+    if (e == cudaSuccess && !layer) {
+        moe::GemmArgs g2{1, d->I, d->H, tiles, ntiles, &hdr->counter[1], &hdr->status, y, s2f, ctas, rev, wait_ns,
+                         stall, 0, nullptr, gate, fused ? at<int32_t>(ws, L.ccnt) : nullptr,
+                         static_cast<__nv_bfloat16 *>(out), d->top_k, d->top_k + sh};
+        g2.trace = trace2;
+        g2.y_f32 = given ? at<float>(ws, L.y) : nullptr;
+        g2.sh_count = sh;
+        g2.sh_T = d->T;
+        g2.sh_rows0 = A;
+        g2.sh_e0 = d->E;
+        e = pairs ? moe::launch_grouped_gemm_2cta(g2, tm_h, tm_wd, tm_wd, at<int32_t>(ws, L.tiles2),
+                                                  at<int32_t>(ws, L.ntiles2), st, &sm2)
+                  : moe::launch_grouped_gemm(g2, tm_h, tm_wd, tm_wd, st, &sm2);
+        if (e == cudaSuccess) e = marks.mark(4, st);
+    }
+    if (e == cudaSuccess && given)
+        e = moe::launch_combine_given(y, true, given->idx, given->w, d->T, d->H, d->E, d->top_k,
+                                      static_cast<__nv_bfloat16 *>(out), st);
+    else if (e == cudaSuccess && !fused)
+        e = moe::launch_combine(y, gate, d->T, d->H, d->top_k, static_cast<__nv_bfloat16 *>(out), st, sh, A);
+    if (e == cudaSuccess) e = marks.mark(5, st);
+    return cuda_status(e);
+}
+
+moe_status_t forward_fp8(const moe_dims_t *d, const void *x, const void *router_w, const float *router_bias,
+                         const GivenRouting *given,
+                             const uint8_t *w_gate_q, const float *w_gate_s, const uint8_t *w_up_q,
+                             const float *w_up_s, const uint8_t *w_down_q, const float *w_down_s, void *out,
+                             void *ws, size_t ws_bytes, void *stream)
+{
+    moe_status_t s = check_dims(d);
+    if (s != MOE_OK) return s;
+    if (d->H % 128 || d->I % 128) return MOE_ERR_INVALID_ARG;
+    if (d->T == 0) return MOE_OK;
+    if (given ? !given->ok() : !router_w || !aligned16(router_w)) return MOE_ERR_INVALID_ARG;
+    if (!x || !w_gate_q || !w_gate_s || !w_up_q || !w_up_s || !w_down_q || !w_down_s || !out)
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(w_gate_q) || !aligned16(w_up_q) ||
+        !aligned16(w_down_q) || !aligned16(out))
+        return MOE_ERR_INVALID_ARG;
+    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return MOE_ERR_WORKSPACE;
+    const moe::WsLayout L = moe::ws_layout(*d, MOE_DTYPE_FP8, 0, given != nullptr);
+    if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int A = d->T * d->top_k;
+    auto *hdr = at<moe::WsHeader>(ws, 0);
+    auto *xs = at<uint8_t>(ws, L.xs);
+    auto *xs_s = at<float>(ws, L.xs_s);
+    auto *h = at<uint8_t>(ws, L.h);
+    auto *h_s = at<float>(ws, L.h_s);
+    auto *y = at<__nv_bfloat16>(ws, L.y);
+    auto *idx = at<int32_t>(ws, L.idx);
+    auto *gate = at<float>(ws, L.gate);
+    auto *s2f = at<int32_t>(ws, L.s2f);
+    auto *tiles = at<int32_t>(ws, L.tiles);
+    auto *ntiles = at<int32_t>(ws, L.ntiles);
+
+    moe::AMaps tm_xs, tm_h;
+    CUtensorMap tm_wg, tm_wu, tm_wd;
+    if (!moe::encode_a_maps(&tm_xs, xs, A, d->H, true) || !encode_3d_u8(&tm_wg, w_gate_q, d->E, d->I, d->H, 128) ||
+        !encode_3d_u8(&tm_wu, w_up_q, d->E, d->I, d->H, 128) || !moe::encode_a_maps(&tm_h, h, A, d->I, true) ||
+        !encode_3d_u8(&tm_wd, w_down_q, d->E, d->H, d->I, 256))
+        return MOE_ERR_CUDA;
+
+    const StageMarks marks;
+    const bool fused = !given && d->T <= moe::kFusedCombineMaxTFp8;  // combine inside the down GEMM
+    cudaError_t e = marks.mark(0, st);
+    if (e == cudaSuccess) e = group_assignments(*d, L, x, router_w, router_bias, given, ws, hdr, marks, st);
+    // x quantised once per token, then its codes gathered into expert order
+    if (e == cudaSuccess)
+        e = moe::launch_quantize_rows(static_cast<const __nv_bfloat16 *>(x), nullptr, 1, d->T, d->H,
+                                      at<uint8_t>(ws, L.xq), at<float>(ws, L.xq_s), st);
+    if (e == cudaSuccess)
+        e = moe::launch_gather_rows_fp8(at<uint8_t>(ws, L.xq), at<float>(ws, L.xq_s), s2f, A, d->H, d->top_k, xs,
+                                        xs_s, st);
+    if (e == cudaSuccess) e = marks.mark(2, st);
+    const int ctas = g_gemm_ctas.load(), rev = g_claim_reverse.load();
+    unsigned long long *trace1 = g_trace.load(), *trace2 = trace1 ? trace1 + 2 * g_trace_ctas.load() : nullptr;
+    const unsigned long long wl = g_wait_ns.load();
+    const uint64_t wait_ns = wl ? wl : 2000000000ull;
+    const int stall = g_stall_test.load();
+    if (e == cudaSuccess) {
+        moe::Fp8GemmArgs g1{0, d->H, d->I, tiles, ntiles, &hdr->counter[0], &hdr->status, xs_s, w_gate_s, w_up_s,
+                            h, h_s, nullptr, nullptr, ctas, rev, wait_ns, stall};
+        g1.trace = trace1;
+        // operands swapped when the groups average at most 64 rows per expert
+        const int sw = g_fp8_swap.load();
+        const bool swap = sw == 1 || (sw == 0 && moe::tile_choice(A, d->E).fp8_swap_ab);
+        e = swap ? moe::launch_grouped_gemm_fp8_swapab(g1, tm_xs, tm_wg, tm_wu, st)
+                 : moe::launch_grouped_gemm_fp8(g1, tm_xs, tm_wg, tm_wu, st);
+    }
+    if (e == cudaSuccess) e = marks.mark(3, st);
+    if (e == cudaSuccess) {
+        moe::Fp8GemmArgs g2{1, d->I, d->H, tiles, ntiles, &hdr->counter[1], &hdr->status, h_s, w_down_s, w_down_s,
+                            nullptr, nullptr, y, s2f, ctas, rev, wait_ns, stall, 0, 1, nullptr, gate,
+                            fused ? at<int32_t>(ws, L.ccnt) : nullptr, static_cast<__nv_bfloat16 *>(out), d->top_k,
+                            2 * d->top_k};
+        g2.trace = trace2;
+        e = moe::launch_grouped_gemm_fp8(g2, tm_h, tm_wd, tm_wd, st);
+    }
+    if (e == cudaSuccess) e = marks.mark(4, st);
+    if (e == cudaSuccess && given)
+        e = moe::launch_combine_given(y, false, given->idx, given->w, d->T, d->H, d->E, d->top_k,
+                                      static_cast<__nv_bfloat16 *>(out), st);
+    else if (e == cudaSuccess && !fused)
+        e = moe::launch_combine(y, gate, d->T, d->H, d->top_k, static_cast<__nv_bfloat16 *>(out), st);
+    if (e == cudaSuccess) e = marks.mark(5, st);
+    return cuda_status(e);
+}
+
+moe_status_t forward_mx(const moe_dims_t *d, const void *x, const void *router_w, const float *router_bias,
+                         const GivenRouting *given,
+                            const uint8_t *w_gate_p, const uint8_t *w_gate_x, const uint8_t *w_up_p,
+                            const uint8_t *w_up_x, const uint8_t *w_down_p, const uint8_t *w_down_x, void *out,
+                            void *ws, size_t ws_bytes, void *stream)
+{
+    moe_status_t s = check_dims(d);
+    if (s != MOE_OK) return s;
+    if (d->H % 512 || d->I % 512) return MOE_ERR_INVALID_ARG;
+    if (d->T == 0) return MOE_OK;
+    if (given ? !given->ok() : !router_w || !aligned16(router_w)) return MOE_ERR_INVALID_ARG;
+    if (!x || !w_gate_p || !w_gate_x || !w_up_p || !w_up_x || !w_down_p || !w_down_x || !out)
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(w_gate_p) || !aligned16(w_up_p) ||
+        !aligned16(w_down_p) || !aligned16(w_gate_x) || !aligned16(w_up_x) || !aligned16(w_down_x) ||
+        !aligned16(out))
+        return MOE_ERR_INVALID_ARG;
+    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return MOE_ERR_WORKSPACE;
+    const moe::WsLayout L = moe::ws_layout(*d, MOE_DTYPE_MX, 0, given != nullptr);
+    if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int A = d->T * d->top_k;
+    auto *hdr = at<moe::WsHeader>(ws, 0);
+    auto *xs = at<uint8_t>(ws, L.xs);
+    auto *xs_x = at<uint8_t>(ws, L.xs_s);
+    auto *h = at<uint8_t>(ws, L.h);
+    auto *h_x = at<uint8_t>(ws, L.h_s);
+    auto *y = at<__nv_bfloat16>(ws, L.y);
+    auto *gate = at<float>(ws, L.gate);
+    auto *s2f = at<int32_t>(ws, L.s2f);
+    auto *tiles = at<int32_t>(ws, L.tiles);
+    auto *ntiles = at<int32_t>(ws, L.ntiles);
+
+    const int ctas = g_gemm_ctas.load(), rev = g_claim_reverse.load();
+    unsigned long long *trace1 = g_trace.load(), *trace2 = trace1 ? trace1 + 2 * g_trace_ctas.load() : nullptr;
+    const unsigned long long wl = g_wait_ns.load();
+    const uint64_t wait_ns = wl ? wl : 2000000000ull;
+    const int stall = g_stall_test.load();
+    moe::MxLaunch g1{0, d->H, d->I, tiles, ntiles, &hdr->counter[0], &hdr->status, h, h_x, nullptr, nullptr,
+                     ctas, rev, wait_ns, stall, trace1};
+    moe::MxLaunch g2{1, d->I, d->H, tiles, ntiles, &hdr->counter[1], &hdr->status, nullptr, nullptr, y, s2f,
+                     ctas, rev, wait_ns, stall, trace2};
+    if (!moe::encode_a_maps(&g1.tmX, xs, A, d->H, true) ||
+        !encode_4d_fp4_pairs(&g1.tmW0, w_gate_p, d->E, d->I, d->H, 128) ||
+        !encode_4d_fp4_pairs(&g1.tmW1, w_up_p, d->E, d->I, d->H, 128) ||
+        !encode_scales_u8(&g1.tmSX, xs_x, 1, A, d->H / 32, 64, 2) ||
+        !encode_scales_u8(&g1.tmSW0, w_gate_x, d->E, d->I, d->H / 32, 128, 3) ||
+        !encode_scales_u8(&g1.tmSW1, w_up_x, d->E, d->I, d->H / 32, 128, 3) ||
+        !moe::encode_a_maps(&g2.tmX, h, A, d->I, true) ||
+        !encode_4d_fp4_pairs(&g2.tmW0, w_down_p, d->E, d->H, d->I, 128) ||
+        !encode_scales_u8(&g2.tmSX, h_x, 1, A, d->I / 32, 64, 2) ||
+        !encode_scales_u8(&g2.tmSW0, w_down_x, d->E, d->H, d->I / 32, 128, 3))
+        return MOE_ERR_CUDA;
+    g2.tmW1 = g2.tmW0;    // the down GEMM's two tiles are rows n0.. and n0+128.. of w_down
+    g2.tmSW1 = g2.tmSW0;
+
+    const StageMarks marks;
+    cudaError_t e = marks.mark(0, st);
+    if (e == cudaSuccess) e = group_assignments(*d, L, x, router_w, router_bias, given, ws, hdr, marks, st);
+    // x quantised once per token, then its codes and scale codes gathered into expert order
+    if (e == cudaSuccess)
+        e = moe::launch_quantize_rows_mx(static_cast<const __nv_bfloat16 *>(x), d->T, d->H, at<uint8_t>(ws, L.xq),
+                                         at<uint8_t>(ws, L.xq_s), st);
+    if (e == cudaSuccess)
+        e = moe::launch_gather_rows_mx(at<uint8_t>(ws, L.xq), at<uint8_t>(ws, L.xq_s), s2f, A, d->H, d->top_k, xs,
+                                       xs_x, st);
+    if (e == cudaSuccess) e = marks.mark(2, st);
+    if (e == cudaSuccess) e = moe::launch_grouped_gemm_mx(g1, st);
+    if (e == cudaSuccess) e = marks.mark(3, st);
+    if (e == cudaSuccess) e = moe::launch_grouped_gemm_mx(g2, st);
+    if (e == cudaSuccess) e = marks.mark(4, st);
+    if (e == cudaSuccess && given)
+        e = moe::launch_combine_given(y, false, given->idx, given->w, d->T, d->H, d->E, d->top_k,
+                                      static_cast<__nv_bfloat16 *>(out), st);
+    else if (e == cudaSuccess)
+        e = moe::launch_combine(y, gate, d->T, d->H, d->top_k, static_cast<__nv_bfloat16 *>(out), st);
+    if (e == cudaSuccess) e = marks.mark(5, st);
+    return cuda_status(e);
+}
+
+}  // namespace
+
 extern "C" {
 
 size_t moe_workspace_size(const moe_dims_t *d, int dtype)
@@ -534,145 +888,8 @@ moe_status_t moe_forward_shared(const moe_dims_t *d, const void *x, const void *
                                 const void *shared_gate, const void *shared_up, const void *shared_down, void *out,
                                 void *ws, size_t ws_bytes, void *stream)
 {
-    moe_status_t s = check_dims(d);
-    if (s != MOE_OK) return s;
-    if (shared_I < 0 || shared_I % d->I != 0) return MOE_ERR_INVALID_ARG;
-    const int sh = shared_I / d->I;  // slices of the shared expert, I columns each
-    if (d->T == 0) return MOE_OK;
-    if (!x || !router_w || !w_gate || !w_up || !w_down || !out) return MOE_ERR_INVALID_ARG;
-    if (!aligned16(x) || !aligned16(router_w) || !aligned16(w_gate) || !aligned16(w_up) || !aligned16(w_down) ||
-        !aligned16(out))
-        return MOE_ERR_INVALID_ARG;
-    if (sh && (!shared_gate || !shared_up || !shared_down || !aligned16(shared_gate) || !aligned16(shared_up) ||
-               !aligned16(shared_down)))
-        return MOE_ERR_INVALID_ARG;
-    if ((int64_t)sh * d->T + (int64_t)d->T * d->top_k > (int64_t)INT32_MAX / 2) return MOE_ERR_UNSUPPORTED;
-    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return MOE_ERR_WORKSPACE;
-    const moe::WsLayout L = moe::ws_layout(*d, MOE_DTYPE_BF16, sh);
-    if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int A = d->T * d->top_k;
-    const int R = A + sh * d->T;  // rows of h and y: the routed assignments, then the shared expert's
-    auto *hdr = at<moe::WsHeader>(ws, 0);
-    auto *xs = at<__nv_bfloat16>(ws, L.xs);
-    auto *h = at<__nv_bfloat16>(ws, L.h);
-    auto *y = at<__nv_bfloat16>(ws, L.y);
-    auto *gate = at<float>(ws, L.gate);
-    auto *s2f = at<int32_t>(ws, L.s2f);
-    auto *tiles = at<int32_t>(ws, L.tiles);
-    auto *ntiles = at<int32_t>(ws, L.ntiles);
-
-    moe::AMaps tm_xs, tm_h;
-    CUtensorMap tm_wg, tm_wu, tm_wd;
-    // pair-of-CTA GEMMs for groups large enough to be compute-bound (on average at
-    // least 768 rows per expert), on the queue's claim modes
-    const int plan = bf16_plan(*d);
-    const bool pairs = plan & MOE_PLAN_PAIR_TILES;
-    if (!moe::encode_a_maps(&tm_xs, xs, A, d->H, false) ||
-        !encode_4d_chunked(&tm_wg, w_gate, d->E, d->I, d->H, 128, 2) ||
-        !encode_4d_chunked(&tm_wu, w_up, d->E, d->I, d->H, 128, 2) ||
-        !moe::encode_a_maps(&tm_h, h, R, d->I, false) ||
-        !encode_4d_chunked(&tm_wd, w_down, d->E, d->H, d->I, pairs ? 128 : 256, 2))
-        return MOE_ERR_CUDA;
-    // the shared expert: x itself as its gate/up A operand, its weights as chunked maps
-    // with the boxes of the routed experts' maps
-    moe::SharedMaps sm1{}, sm2{};
-    if (sh && (!moe::encode_a_maps(&sm1.x, x, d->T, d->H, false) ||
-               !moe::encode_sw128_chunked_bf16(&sm1.b0, shared_gate, shared_I, d->H, 128, 2) ||
-               !moe::encode_sw128_chunked_bf16(&sm1.b1, shared_up, shared_I, d->H, 128, 2) ||
-               !moe::encode_sw128_chunked_bf16(&sm2.b0, shared_down, d->H, shared_I, pairs ? 128 : 256, 2)))
-        return MOE_ERR_CUDA;
-    // gate/up A rows straight from x: one-row boxes for tile::gather4, the token of
-    // sorted row r being sorted_to_flat[r] / k
-    const bool direct = plan & MOE_PLAN_DIRECT_A;
-    if (direct && !encode_2d(&sm1.xg, x, d->T, d->H, 1)) return MOE_ERR_CUDA;
-    // the tile list is then the output of the kernel just before the gate/up GEMM
-    // when the router and the grouping are one launch
-    const int tiles_first = direct && (plan & MOE_PLAN_SMALL_ROUTER) ? 1 : 0;
-
-    const StageMarks marks;
-    const bool fused = plan & MOE_PLAN_FUSED_COMBINE;  // combine inside the down GEMM
-    cudaError_t e = marks.mark(0, st);
-    if (e == cudaSuccess && !moe::small_route_permute_ok(*d))  // else the router's kernels clear them
-        e = cudaMemsetAsync(hdr, 0, L.clear_bytes, st);          // header + combine counts
-    if (e == cudaSuccess) e = route_and_permute(*d, L, x, router_w, router_bias, ws, hdr, marks, st);
-    if (e == cudaSuccess && !direct)
-        e = moe::launch_gather_rows(static_cast<const __nv_bfloat16 *>(x), at<int32_t>(ws, L.f2s), d->T, d->H,
-                                    d->top_k, xs, st);
-    if (e == cudaSuccess) e = marks.mark(2, st);
-    const int ctas = g_gemm_ctas.load(), rev = g_claim_reverse.load();
-    unsigned long long *trace1 = g_trace.load(), *trace2 = trace1 ? trace1 + 2 * g_trace_ctas.load() : nullptr;
-    const unsigned long long wl = g_wait_ns.load();
-    const uint64_t wait_ns = wl ? wl : 2000000000ull;
-    const int stall = g_stall_test.load();
-    // the gate/up and the down GEMM in one persistent launch (readiness counters per
-    // m-tile hand h from one to the other)
-    const bool layer = plan & MOE_PLAN_LAYER_GEMM;
-    if (e == cudaSuccess && layer) {
-        moe::GemmArgs gl{3, d->H, d->I, tiles, ntiles, &hdr->counter[0], &hdr->status, h, s2f, ctas, rev, wait_ns,
-                         stall, 0, nullptr, gate, fused ? at<int32_t>(ws, L.ccnt) : nullptr,
-                         static_cast<__nv_bfloat16 *>(out), d->top_k, d->top_k + sh};
-        gl.trace = trace1;
-        gl.sh_count = sh;
-        gl.sh_T = d->T;
-        gl.sh_rows0 = A;
-        gl.sh_e0 = d->E;
-        gl.K2 = d->I;
-        gl.N2 = d->H;
-        gl.out2 = y;
-        gl.ready = at<int32_t>(ws, L.ready);
-        if (direct) {
-            gl.a_rows = s2f;
-            gl.a_div = d->top_k;
-            gl.a_tokens = d->T;
-            gl.tiles_first = tiles_first;
-        }
-        moe::LayerMaps lm{};
-        lm.h = tm_h;
-        lm.wd = tm_wd;
-        lm.wd_sh = sm2.b0;
-        e = pairs ? moe::launch_grouped_gemm_2cta(gl, tm_xs, tm_wg, tm_wu, at<int32_t>(ws, L.tiles2),
-                                                  at<int32_t>(ws, L.ntiles2), st, &sm1, &lm)
-                  : moe::launch_grouped_gemm(gl, tm_xs, tm_wg, tm_wu, st, &sm1, &lm);
-        if (e == cudaSuccess) e = marks.mark(3, st);
-        if (e == cudaSuccess) e = marks.mark(4, st);
-    }
-    if (e == cudaSuccess && !layer) {
-        moe::GemmArgs g1{0, d->H, d->I, tiles, ntiles, &hdr->counter[0], &hdr->status, h, nullptr, ctas, rev, wait_ns, stall};
-        g1.trace = trace1;
-        g1.sh_count = sh;
-        g1.sh_T = d->T;
-        g1.sh_rows0 = A;
-        g1.sh_e0 = d->E;
-        if (direct) {
-            g1.a_rows = s2f;
-            g1.a_div = d->top_k;
-            g1.a_tokens = d->T;
-            g1.tiles_first = tiles_first;
-        }
-        e = pairs ? moe::launch_grouped_gemm_2cta(g1, tm_xs, tm_wg, tm_wu, at<int32_t>(ws, L.tiles2),
-                                                  at<int32_t>(ws, L.ntiles2), st, &sm1)
-                  : moe::launch_grouped_gemm(g1, tm_xs, tm_wg, tm_wu, st, &sm1);
-        if (e == cudaSuccess) e = marks.mark(3, st);
-    }
-    if (e == cudaSuccess && !layer) {
-        moe::GemmArgs g2{1, d->I, d->H, tiles, ntiles, &hdr->counter[1], &hdr->status, y, s2f, ctas, rev, wait_ns,
-                         stall, 0, nullptr, gate, fused ? at<int32_t>(ws, L.ccnt) : nullptr,
-                         static_cast<__nv_bfloat16 *>(out), d->top_k, d->top_k + sh};
-        g2.trace = trace2;
-        g2.sh_count = sh;
-        g2.sh_T = d->T;
-        g2.sh_rows0 = A;
-        g2.sh_e0 = d->E;
-        e = pairs ? moe::launch_grouped_gemm_2cta(g2, tm_h, tm_wd, tm_wd, at<int32_t>(ws, L.tiles2),
-                                                  at<int32_t>(ws, L.ntiles2), st, &sm2)
-                  : moe::launch_grouped_gemm(g2, tm_h, tm_wd, tm_wd, st, &sm2);
-        if (e == cudaSuccess) e = marks.mark(4, st);
-    }
-    if (e == cudaSuccess && !fused)
-        e = moe::launch_combine(y, gate, d->T, d->H, d->top_k, static_cast<__nv_bfloat16 *>(out), st, sh, A);
-    if (e == cudaSuccess) e = marks.mark(5, st);
-    return cuda_status(e);
+    return forward_bf16(d, x, router_w, router_bias, nullptr, w_gate, w_up, w_down, shared_I, shared_gate, shared_up,
+                        shared_down, out, ws, ws_bytes, stream);
 }
 
 moe_status_t moe_quantize_rows_fp8(int32_t R, int32_t K, const void *a, uint8_t *q, float *s, void *stream)
@@ -689,82 +906,7 @@ moe_status_t moe_forward_fp8(const moe_dims_t *d, const void *x, const void *rou
                              const float *w_up_s, const uint8_t *w_down_q, const float *w_down_s, void *out,
                              void *ws, size_t ws_bytes, void *stream)
 {
-    moe_status_t s = check_dims(d);
-    if (s != MOE_OK) return s;
-    if (d->H % 128 || d->I % 128) return MOE_ERR_INVALID_ARG;
-    if (d->T == 0) return MOE_OK;
-    if (!x || !router_w || !w_gate_q || !w_gate_s || !w_up_q || !w_up_s || !w_down_q || !w_down_s || !out)
-        return MOE_ERR_INVALID_ARG;
-    if (!aligned16(x) || !aligned16(router_w) || !aligned16(w_gate_q) || !aligned16(w_up_q) ||
-        !aligned16(w_down_q) || !aligned16(out))
-        return MOE_ERR_INVALID_ARG;
-    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return MOE_ERR_WORKSPACE;
-    const moe::WsLayout L = moe::ws_layout(*d, MOE_DTYPE_FP8);
-    if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int A = d->T * d->top_k;
-    auto *hdr = at<moe::WsHeader>(ws, 0);
-    auto *xs = at<uint8_t>(ws, L.xs);
-    auto *xs_s = at<float>(ws, L.xs_s);
-    auto *h = at<uint8_t>(ws, L.h);
-    auto *h_s = at<float>(ws, L.h_s);
-    auto *y = at<__nv_bfloat16>(ws, L.y);
-    auto *idx = at<int32_t>(ws, L.idx);
-    auto *gate = at<float>(ws, L.gate);
-    auto *s2f = at<int32_t>(ws, L.s2f);
-    auto *tiles = at<int32_t>(ws, L.tiles);
-    auto *ntiles = at<int32_t>(ws, L.ntiles);
-
-    moe::AMaps tm_xs, tm_h;
-    CUtensorMap tm_wg, tm_wu, tm_wd;
-    if (!moe::encode_a_maps(&tm_xs, xs, A, d->H, true) || !encode_3d_u8(&tm_wg, w_gate_q, d->E, d->I, d->H, 128) ||
-        !encode_3d_u8(&tm_wu, w_up_q, d->E, d->I, d->H, 128) || !moe::encode_a_maps(&tm_h, h, A, d->I, true) ||
-        !encode_3d_u8(&tm_wd, w_down_q, d->E, d->H, d->I, 256))
-        return MOE_ERR_CUDA;
-
-    const StageMarks marks;
-    const bool fused = d->T <= moe::kFusedCombineMaxTFp8;  // combine inside the down GEMM
-    cudaError_t e = marks.mark(0, st);
-    if (e == cudaSuccess && !moe::small_route_permute_ok(*d))  // else the router's kernels clear them
-        e = cudaMemsetAsync(hdr, 0, L.clear_bytes, st);          // header + combine counts
-    if (e == cudaSuccess) e = route_and_permute(*d, L, x, router_w, router_bias, ws, hdr, marks, st);
-    // x quantised once per token, then its codes gathered into expert order
-    if (e == cudaSuccess)
-        e = moe::launch_quantize_rows(static_cast<const __nv_bfloat16 *>(x), nullptr, 1, d->T, d->H,
-                                      at<uint8_t>(ws, L.xq), at<float>(ws, L.xq_s), st);
-    if (e == cudaSuccess)
-        e = moe::launch_gather_rows_fp8(at<uint8_t>(ws, L.xq), at<float>(ws, L.xq_s), s2f, A, d->H, d->top_k, xs,
-                                        xs_s, st);
-    if (e == cudaSuccess) e = marks.mark(2, st);
-    const int ctas = g_gemm_ctas.load(), rev = g_claim_reverse.load();
-    unsigned long long *trace1 = g_trace.load(), *trace2 = trace1 ? trace1 + 2 * g_trace_ctas.load() : nullptr;
-    const unsigned long long wl = g_wait_ns.load();
-    const uint64_t wait_ns = wl ? wl : 2000000000ull;
-    const int stall = g_stall_test.load();
-    if (e == cudaSuccess) {
-        moe::Fp8GemmArgs g1{0, d->H, d->I, tiles, ntiles, &hdr->counter[0], &hdr->status, xs_s, w_gate_s, w_up_s,
-                            h, h_s, nullptr, nullptr, ctas, rev, wait_ns, stall};
-        g1.trace = trace1;
-        // operands swapped when the groups average at most 64 rows per expert
-        const int sw = g_fp8_swap.load();
-        const bool swap = sw == 1 || (sw == 0 && moe::tile_choice(A, d->E).fp8_swap_ab);
-        e = swap ? moe::launch_grouped_gemm_fp8_swapab(g1, tm_xs, tm_wg, tm_wu, st)
-                 : moe::launch_grouped_gemm_fp8(g1, tm_xs, tm_wg, tm_wu, st);
-    }
-    if (e == cudaSuccess) e = marks.mark(3, st);
-    if (e == cudaSuccess) {
-        moe::Fp8GemmArgs g2{1, d->I, d->H, tiles, ntiles, &hdr->counter[1], &hdr->status, h_s, w_down_s, w_down_s,
-                            nullptr, nullptr, y, s2f, ctas, rev, wait_ns, stall, 0, 1, nullptr, gate,
-                            fused ? at<int32_t>(ws, L.ccnt) : nullptr, static_cast<__nv_bfloat16 *>(out), d->top_k,
-                            2 * d->top_k};
-        g2.trace = trace2;
-        e = moe::launch_grouped_gemm_fp8(g2, tm_h, tm_wd, tm_wd, st);
-    }
-    if (e == cudaSuccess) e = marks.mark(4, st);
-    if (e == cudaSuccess && !fused)
-        e = moe::launch_combine(y, gate, d->T, d->H, d->top_k, static_cast<__nv_bfloat16 *>(out), st);
-    if (e == cudaSuccess) e = marks.mark(5, st);
-    return cuda_status(e);
+    return forward_fp8(d, x, router_w, router_bias, nullptr, w_gate_q, w_gate_s, w_up_q, w_up_s, w_down_q, w_down_s, out, ws, ws_bytes, stream);
 }
 
 moe_status_t moe_quantize_rows_mx(int32_t R, int32_t K, const void *a, uint8_t *q, uint8_t *x, void *stream)
@@ -781,75 +923,41 @@ moe_status_t moe_forward_mx(const moe_dims_t *d, const void *x, const void *rout
                             const uint8_t *w_up_x, const uint8_t *w_down_p, const uint8_t *w_down_x, void *out,
                             void *ws, size_t ws_bytes, void *stream)
 {
-    moe_status_t s = check_dims(d);
-    if (s != MOE_OK) return s;
-    if (d->H % 512 || d->I % 512) return MOE_ERR_INVALID_ARG;
-    if (d->T == 0) return MOE_OK;
-    if (!x || !router_w || !w_gate_p || !w_gate_x || !w_up_p || !w_up_x || !w_down_p || !w_down_x || !out)
-        return MOE_ERR_INVALID_ARG;
-    if (!aligned16(x) || !aligned16(router_w) || !aligned16(w_gate_p) || !aligned16(w_up_p) ||
-        !aligned16(w_down_p) || !aligned16(w_gate_x) || !aligned16(w_up_x) || !aligned16(w_down_x) ||
-        !aligned16(out))
-        return MOE_ERR_INVALID_ARG;
-    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return MOE_ERR_WORKSPACE;
-    const moe::WsLayout L = moe::ws_layout(*d, MOE_DTYPE_MX);
-    if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int A = d->T * d->top_k;
-    auto *hdr = at<moe::WsHeader>(ws, 0);
-    auto *xs = at<uint8_t>(ws, L.xs);
-    auto *xs_x = at<uint8_t>(ws, L.xs_s);
-    auto *h = at<uint8_t>(ws, L.h);
-    auto *h_x = at<uint8_t>(ws, L.h_s);
-    auto *y = at<__nv_bfloat16>(ws, L.y);
-    auto *gate = at<float>(ws, L.gate);
-    auto *s2f = at<int32_t>(ws, L.s2f);
-    auto *tiles = at<int32_t>(ws, L.tiles);
-    auto *ntiles = at<int32_t>(ws, L.ntiles);
+    return forward_mx(d, x, router_w, router_bias, nullptr, w_gate_p, w_gate_x, w_up_p, w_up_x, w_down_p, w_down_x, out, ws, ws_bytes, stream);
+}
 
-    const int ctas = g_gemm_ctas.load(), rev = g_claim_reverse.load();
-    unsigned long long *trace1 = g_trace.load(), *trace2 = trace1 ? trace1 + 2 * g_trace_ctas.load() : nullptr;
-    const unsigned long long wl = g_wait_ns.load();
-    const uint64_t wait_ns = wl ? wl : 2000000000ull;
-    const int stall = g_stall_test.load();
-    moe::MxLaunch g1{0, d->H, d->I, tiles, ntiles, &hdr->counter[0], &hdr->status, h, h_x, nullptr, nullptr,
-                     ctas, rev, wait_ns, stall, trace1};
-    moe::MxLaunch g2{1, d->I, d->H, tiles, ntiles, &hdr->counter[1], &hdr->status, nullptr, nullptr, y, s2f,
-                     ctas, rev, wait_ns, stall, trace2};
-    if (!moe::encode_a_maps(&g1.tmX, xs, A, d->H, true) ||
-        !encode_4d_fp4_pairs(&g1.tmW0, w_gate_p, d->E, d->I, d->H, 128) ||
-        !encode_4d_fp4_pairs(&g1.tmW1, w_up_p, d->E, d->I, d->H, 128) ||
-        !encode_scales_u8(&g1.tmSX, xs_x, 1, A, d->H / 32, 64, 2) ||
-        !encode_scales_u8(&g1.tmSW0, w_gate_x, d->E, d->I, d->H / 32, 128, 3) ||
-        !encode_scales_u8(&g1.tmSW1, w_up_x, d->E, d->I, d->H / 32, 128, 3) ||
-        !moe::encode_a_maps(&g2.tmX, h, A, d->I, true) ||
-        !encode_4d_fp4_pairs(&g2.tmW0, w_down_p, d->E, d->H, d->I, 128) ||
-        !encode_scales_u8(&g2.tmSX, h_x, 1, A, d->I / 32, 64, 2) ||
-        !encode_scales_u8(&g2.tmSW0, w_down_x, d->E, d->H, d->I / 32, 128, 3))
-        return MOE_ERR_CUDA;
-    g2.tmW1 = g2.tmW0;    // the down GEMM's two tiles are rows n0.. and n0+128.. of w_down
-    g2.tmSW1 = g2.tmSW0;
+size_t moe_experts_workspace_size(const moe_dims_t *d, int dtype)
+{
+    return moe_workspace_size(d, dtype) ? moe::ws_layout(*d, dtype, 0, true).total : 0;
+}
 
-    const StageMarks marks;
-    cudaError_t e = marks.mark(0, st);
-    if (e == cudaSuccess && !moe::small_route_permute_ok(*d))  // else the router's kernels clear them
-        e = cudaMemsetAsync(hdr, 0, L.clear_bytes, st);
-    if (e == cudaSuccess) e = route_and_permute(*d, L, x, router_w, router_bias, ws, hdr, marks, st);
-    // x quantised once per token, then its codes and scale codes gathered into expert order
-    if (e == cudaSuccess)
-        e = moe::launch_quantize_rows_mx(static_cast<const __nv_bfloat16 *>(x), d->T, d->H, at<uint8_t>(ws, L.xq),
-                                         at<uint8_t>(ws, L.xq_s), st);
-    if (e == cudaSuccess)
-        e = moe::launch_gather_rows_mx(at<uint8_t>(ws, L.xq), at<uint8_t>(ws, L.xq_s), s2f, A, d->H, d->top_k, xs,
-                                       xs_x, st);
-    if (e == cudaSuccess) e = marks.mark(2, st);
-    if (e == cudaSuccess) e = moe::launch_grouped_gemm_mx(g1, st);
-    if (e == cudaSuccess) e = marks.mark(3, st);
-    if (e == cudaSuccess) e = moe::launch_grouped_gemm_mx(g2, st);
-    if (e == cudaSuccess) e = marks.mark(4, st);
-    if (e == cudaSuccess) e = moe::launch_combine(y, gate, d->T, d->H, d->top_k, static_cast<__nv_bfloat16 *>(out), st);
-    if (e == cudaSuccess) e = marks.mark(5, st);
-    return cuda_status(e);
+moe_status_t moe_experts(const moe_dims_t *d, const void *x, const int32_t *topk_idx, const float *topk_w,
+                         const void *w_gate, const void *w_up, const void *w_down, void *out, void *ws,
+                         size_t ws_bytes, void *stream)
+{
+    const GivenRouting given{topk_idx, topk_w};
+    return forward_bf16(d, x, nullptr, nullptr, &given, w_gate, w_up, w_down, 0, nullptr, nullptr, nullptr, out, ws,
+                        ws_bytes, stream);
+}
+
+moe_status_t moe_experts_fp8(const moe_dims_t *d, const void *x, const int32_t *topk_idx, const float *topk_w,
+                             const uint8_t *w_gate_q, const float *w_gate_s, const uint8_t *w_up_q,
+                             const float *w_up_s, const uint8_t *w_down_q, const float *w_down_s, void *out, void *ws,
+                             size_t ws_bytes, void *stream)
+{
+    const GivenRouting given{topk_idx, topk_w};
+    return forward_fp8(d, x, nullptr, nullptr, &given, w_gate_q, w_gate_s, w_up_q, w_up_s, w_down_q, w_down_s, out,
+                       ws, ws_bytes, stream);
+}
+
+moe_status_t moe_experts_mx(const moe_dims_t *d, const void *x, const int32_t *topk_idx, const float *topk_w,
+                            const uint8_t *w_gate_p, const uint8_t *w_gate_x, const uint8_t *w_up_p,
+                            const uint8_t *w_up_x, const uint8_t *w_down_p, const uint8_t *w_down_x, void *out,
+                            void *ws, size_t ws_bytes, void *stream)
+{
+    const GivenRouting given{topk_idx, topk_w};
+    return forward_mx(d, x, nullptr, nullptr, &given, w_gate_p, w_gate_x, w_up_p, w_up_x, w_down_p, w_down_x, out, ws,
+                      ws_bytes, stream);
 }
 
 int32_t moe_forward_plan(const moe_dims_t *d, int dtype)

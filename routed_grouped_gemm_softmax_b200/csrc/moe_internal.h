@@ -45,7 +45,9 @@ inline int perm_warps(int E)
 
 // Workspace regions; with fp8 the sorted activations and h are e4m3 codes plus
 // one fp32 scale per 128 columns, and x is quantised per token before the gather.
-inline WsLayout ws_layout(const moe_dims_t &d, int dtype = MOE_DTYPE_BF16, int sh_count = 0)
+// `given`: the layer on a routing that is given (moe_experts), without the router's
+// regions and, in bf16, with fp32 per-assignment outputs.
+inline WsLayout ws_layout(const moe_dims_t &d, int dtype = MOE_DTYPE_BF16, int sh_count = 0, bool given = false)
 {
     const bool fp8 = dtype == MOE_DTYPE_FP8, mx = dtype == MOE_DTYPE_MX;
     // bytes of the scales of n activation values: fp32 per 128 (fp8), e8m0 per 32 (MX)
@@ -72,16 +74,16 @@ inline WsLayout ws_layout(const moe_dims_t &d, int dtype = MOE_DTYPE_BF16, int s
         o = align_up(o + bytes, 1024);
         return at;
     };
-    L.logits = take(static_cast<size_t>(d.T) * d.E * 4 * kRouterKSplitMax);
-    L.wrt = take(static_cast<size_t>(d.E) * d.H * 2);
-    L.wsq = take(static_cast<size_t>(d.E) * 4 * ((d.H + 255) / 256));  // partial squared norms
-    const bool tc_router = d.T > 32;  // the certified router's candidate lists
+    L.logits = take(given ? 0 : static_cast<size_t>(d.T) * d.E * 4 * kRouterKSplitMax);
+    L.wrt = take(given ? 0 : static_cast<size_t>(d.E) * d.H * 2);
+    L.wsq = take(given ? 0 : static_cast<size_t>(d.E) * 4 * ((d.H + 255) / 256));  // partial squared norms
+    const bool tc_router = d.T > 32 && !given;  // the certified router's candidate lists
     L.rncand = take(tc_router ? static_cast<size_t>(d.T) * 4 : 0);
     L.rlist = take(tc_router ? static_cast<size_t>(d.T) * d.E * 16 : 0);
     L.blk_cnt = take(static_cast<size_t>(L.nb > 0 ? L.nb : 1) * d.E * 4);
     L.blk_base = take(static_cast<size_t>(L.nb > 0 ? L.nb : 1) * d.E * 4);
-    L.idx = take(A * 4);
-    L.gate = take(A * 4);
+    L.idx = take(given ? 0 : A * 4);
+    L.gate = take(given ? 0 : A * 4);
     L.offsets = take(static_cast<size_t>(d.E + 1) * 4);
     L.s2f = take(A * 4);
     L.f2s = take(A * 4);
@@ -95,7 +97,7 @@ inline WsLayout ws_layout(const moe_dims_t &d, int dtype = MOE_DTYPE_BF16, int s
     L.xs_s = take(act_scales(A * d.H));
     L.h = take((A + SR) * d.I * (q8 ? 1 : 2));
     L.h_s = take(act_scales(A * d.I));
-    L.y = take((A + SR) * d.H * 2);
+    L.y = take((A + SR) * d.H * (given && !q8 ? 4 : 2));
     L.total = o;
     return L;
 }
@@ -139,11 +141,14 @@ cudaError_t launch_route_permute_small(const moe_dims_t &d, const __nv_bfloat16 
                                        int32_t *offsets, int32_t *s2f, int32_t *f2s, int32_t *tiles,
                                        int32_t *ntiles, WsHeader *hdr, int32_t *ccnt, int nccnt, cudaStream_t st);
 
-// Also writes the 2 x 128-row pair tiles when tiles2 is non-null.
+// Also writes the 2 x 128-row pair tiles when tiles2 is non-null.  none_ok: entries of -1
+// are assignments to no expert, skipped without an error; f2s of every skipped entry
+// is -1 (else it is left as it was); s2f past the last sorted row is 0.
 cudaError_t launch_permute(const moe_dims_t &d, const WsLayout &L, const int32_t *idx,
                            int32_t *blk_cnt, int32_t *blk_base, int32_t *offsets, int32_t *s2f,
                            int32_t *f2s, int32_t *tiles, int32_t *ntiles, WsHeader *hdr,
-                           cudaStream_t st, int32_t *tiles2 = nullptr, int32_t *ntiles2 = nullptr);
+                           cudaStream_t st, int32_t *tiles2 = nullptr, int32_t *ntiles2 = nullptr,
+                           bool none_ok = false);
 
 // xs[f2s[f]] = x[f / k] for every assignment f = t*k + j (a warp per assignment, flat order).
 cudaError_t launch_gather_rows(const __nv_bfloat16 *x, const int32_t *f2s, int T, int H, int top_k,
@@ -218,6 +223,9 @@ struct GemmArgs {
     // The tile list is written by the kernel launched just before this one (no other
     // kernel in between), so it is read only after the programmatic-dependency wait.
     int tiles_first;
+    // Down items with y_f32 non-null: y rows are written there in fp32 instead of in bf16 to
+    // out (mode 1) or out2 (mode 3); no fused combine.
+    float *y_f32;
 };
 
 // Tensor maps of the down half of the fused layer GEMM (mode 3): h as its A operand
@@ -357,6 +365,10 @@ cudaError_t tc_router_logits(const __nv_bfloat16 *x, const __nv_bfloat16 *wrt, i
 // plus, with sh_count > 0, the shared expert's rows y[sh_rows0 + s * T + t] at gate 1.
 cudaError_t launch_combine(const __nv_bfloat16 *y, const float *gate, int T, int H, int top_k,
                            __nv_bfloat16 *out, cudaStream_t st, int sh_count = 0, int sh_rows0 = 0);
+// The same sum on a routing that is given: slots whose index is outside [0, E) have no y
+// row and are skipped.  y is fp32 (y_f32 true) or bf16.
+cudaError_t launch_combine_given(const void *y, bool y_f32, const int32_t *idx, const float *w, int T, int H, int E,
+                                 int top_k, __nv_bfloat16 *out, cudaStream_t st);
 // Scored routing of given logits (route_scored.cu): rows of E logits `ld` elements
 // apart, fp32 or (bf16 = true) bf16.
 struct ScoredArgs {

@@ -27,7 +27,7 @@ __device__ __forceinline__ void record_status(int32_t *status, int code)
 }
 
 __global__ void perm_count_kernel(const int32_t *__restrict__ idx, int A, int E, int chunk,
-                                  int32_t *__restrict__ blk_cnt, int32_t *status)
+                                  int32_t *__restrict__ blk_cnt, int32_t *status, int none_ok)
 {
     pdl_wait();
     pdl_trigger();
@@ -40,7 +40,7 @@ __global__ void perm_count_kernel(const int32_t *__restrict__ idx, int A, int E,
         const int e = idx[f];
         if (e >= 0 && e < E)
             atomicAdd(&hist[e], 1);
-        else
+        else if (!(none_ok && e == -1))
             record_status(status, MOE_ERR_BAD_INDEX);
     }
     __syncthreads();
@@ -130,7 +130,7 @@ perm_scan_kernel(int E, int nb, const int32_t *__restrict__ blk_cnt, int32_t *__
 
 __global__ void perm_scatter_kernel(const int32_t *__restrict__ idx, int A, int E,
                                     const int32_t *__restrict__ blk_base, int32_t *__restrict__ s2f,
-                                    int32_t *__restrict__ f2s)
+                                    int32_t *__restrict__ f2s, int none_ok, const int32_t *__restrict__ offsets)
 {
     pdl_wait();
     pdl_trigger();
@@ -142,12 +142,17 @@ __global__ void perm_scatter_kernel(const int32_t *__restrict__ idx, int A, int 
     const int f = blockIdx.x * blockDim.x + threadIdx.x;
     const int e = f < A ? idx[f] : -1;
     const bool valid = e >= 0 && e < E;
+    // skipped entries leave the tail of s2f without a row: flat row 0, which exists
+    if (none_ok && f < A && f >= offsets[E]) s2f[f] = 0;
     const unsigned peers = __match_any_sync(0xffffffffu, valid ? e : -1);
     const unsigned lower = (1u << lane) - 1u;
     const int rank = __popc(peers & lower);
     if (valid && rank == 0) wcnt[warp * E + e] = __popc(peers);
     __syncthreads();
-    if (!valid) return;
+    if (!valid) {
+        if (none_ok && f < A) f2s[f] = -1;
+        return;
+    }
     int prior = 0;
     for (int w = 0; w < warp; ++w) prior += wcnt[w * E + e];
     const int pos = blk_base[(size_t)blockIdx.x * E + e] + prior + rank;
@@ -181,17 +186,17 @@ __global__ void gather_rows_kernel(const __nv_bfloat16 *__restrict__ x,
 cudaError_t launch_permute(const moe_dims_t &d, const WsLayout &L, const int32_t *idx,
                            int32_t *blk_cnt, int32_t *blk_base, int32_t *offsets, int32_t *s2f,
                            int32_t *f2s, int32_t *tiles, int32_t *ntiles, WsHeader *hdr,
-                           cudaStream_t st, int32_t *tiles2, int32_t *ntiles2)
+                           cudaStream_t st, int32_t *tiles2, int32_t *ntiles2, bool none_ok)
 {
     const int A = d.T * d.top_k, E = d.E;
     cudaError_t e = launch_pdl(perm_count_kernel, dim3(L.nb), dim3(256), E * sizeof(int), st, idx, A, E, L.chunk,
-                               blk_cnt, hdr ? &hdr->status : nullptr);
+                               blk_cnt, hdr ? &hdr->status : nullptr, (int)none_ok);
     if (e == cudaSuccess)
         e = launch_pdl(perm_scan_kernel, dim3(1), dim3(1024), 0, st, E, L.nb, blk_cnt, blk_base, offsets, tiles,
                        ntiles, hdr ? hdr->counter : nullptr, hdr ? 7 : 0, tiles2, ntiles2);
     if (e == cudaSuccess)
         e = launch_pdl(perm_scatter_kernel, dim3(L.nb), dim3(L.chunk), (size_t)(L.chunk / 32) * E * sizeof(int), st,
-                       idx, A, E, blk_base, s2f, f2s);
+                       idx, A, E, blk_base, s2f, f2s, (int)none_ok, offsets);
     return e;
 }
 

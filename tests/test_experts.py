@@ -1,0 +1,259 @@
+"""moe_experts (and its fp8 and MX forms): the experts' products on a given routing, against the
+formula in 64 bits and against the routed forwards; and the scored router, the dense product and
+the experts together, as one layer."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from routed_grouped_gemm_softmax_b200 import api, build
+
+
+def test_host_refusals():
+    build.build()
+    L = api.lib()
+    buf = ctypes.create_string_buffer(8192)
+    p = (ctypes.addressof(buf) + 255) // 256 * 256
+    d = api.dims(4, 512, 512, 8, 2)
+    b = ctypes.byref
+    for dtype in (0, 1, 2):
+        n = L.moe_experts_workspace_size(b(d), dtype)
+        assert 0 < n and n % 1024 == 0
+    assert L.moe_experts_workspace_size(b(d), 3) == 0
+    assert L.moe_experts_workspace_size(b(api.dims(4, 512, 512, 8, 9)), 0) == 0
+    assert L.moe_experts_workspace_size(b(api.dims(4, 256, 512, 8, 2)), 2) == 0
+    forms = [(L.moe_experts, 3), (L.moe_experts_fp8, 6), (L.moe_experts_mx, 6)]
+    for fn, nw in forms:
+        big = 1 << 40
+        good = [b(d), p, p, p] + [p] * nw + [p, p, 1024, None]
+        assert fn(*good) == 3                                   # a workspace that is too small
+        assert fn(*(good[:-3] + [p + 16, big, None])) == 3      # ... or misaligned
+        assert fn(*(good[:-3] + [None, big, None])) == 3
+        for i in range(1, 5 + nw):                              # every pointer is needed
+            assert fn(*(good[:i] + [None] + good[i + 1:])) == 1, i
+        assert fn(*(good[:1] + [p + 8] + good[2:])) == 1
+        assert fn(*(good[:2] + [p + 2] + good[3:])) == 1 and fn(*(good[:3] + [p + 2] + good[4:])) == 1
+        assert fn(*([None] + good[1:])) == 1
+        assert fn(*([b(api.dims(4, 512, 512, 8, 0))] + good[1:])) == 1
+        assert fn(*([b(api.dims(0, 512, 512, 8, 2))] + [None] * (len(good) - 3) + [0, None])) == 0
+
+
+def rnd(shape, seed, std=1.0, dtype=torch.bfloat16):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(*shape, generator=g, device="cuda") * std).to(dtype)
+
+
+def weights(E, H, I):
+    return rnd((E, I, H), 2, H ** -0.5), rnd((E, I, H), 3, H ** -0.5), rnd((E, H, I), 4, I ** -0.5)
+
+
+def routing(T, E, k, seed=5, empty=0.0):
+    g = torch.Generator().manual_seed(seed)
+    idx = torch.randint(0, E, (T, k), generator=g, dtype=torch.int32)  # an expert may come twice
+    idx[torch.rand(T, k, generator=g) < empty] = -1
+    return idx.cuda(), torch.randn(T, k, generator=g).cuda()
+
+
+def check(out, x, idx, w, w_gate, w_up, w_down):
+    H, E, I = x.shape[1], w_gate.shape[0], w_gate.shape[1]
+    y = torch.zeros(x.shape, dtype=torch.float64, device="cuda")
+    err = torch.zeros_like(y)
+    eps = 2.0 ** -8  # one rounding to bf16
+    for e in range(E):
+        t, j = (idx == e).nonzero(as_tuple=True)
+        if not t.numel():
+            continue
+        X = x[t].double()
+        a, u = X @ w_gate[e].double().T, X @ w_up[e].double().T
+        # fp32 sums of H exact products in any order, truncated: at most H steps of 2^-23 of the magnitudes
+        da = H * 2.0 ** -23 * (X.abs() @ w_gate[e].double().abs().T)
+        du = H * 2.0 ** -23 * (X.abs() @ w_up[e].double().abs().T)
+        s = a / (1 + torch.exp(-a))
+        # silu: slope at most 1.1, __expf within 2 + 1.17 |a| units in the last place, a division
+        ds = 1.1 * da + (8 + 2 * a.abs()) * 2.0 ** -23 * s.abs()
+        h = s * u
+        dh = ds * u.abs() + s.abs() * du + ds * du + 2.0 ** -24 * h.abs()
+        dh = dh + eps * (h.abs() + dh)
+        D = w_down[e].double().T
+        g = w[t, j].double()[:, None]
+        y.index_add_(0, t, g * (h @ D))
+        err.index_add_(0, t, g.abs() * (dh @ D.abs() + I * 2.0 ** -23 * ((h.abs() + dh) @ D.abs())))
+        err.index_add_(0, t, (idx.shape[1] + 1) * 2.0 ** -24 * (g * (h @ D)).abs())
+    tol = err * (1 + eps) + eps * y.abs()
+    d = (out.double() - y).abs()
+    bad = ~(d <= tol)
+    assert not bad.any(), f"{int(bad.sum())} of {bad.numel()}, first {bad.nonzero()[0].tolist()}"
+
+
+SHAPES = [(1, 64, 64, 1, 1), (1, 256, 128, 8, 2), (3, 128, 192, 5, 5), (16, 512, 256, 64, 8), (33, 192, 64, 60, 4),
+          (64, 256, 512, 8, 2), (300, 320, 128, 16, 3), (640, 256, 128, 4, 2), (2100, 128, 128, 2, 2), (40, 64, 64, 300, 12)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,H,I,E,k", SHAPES)
+@pytest.mark.parametrize("empty", [0.0, 0.4, 1.0])
+def test_against_64_bits(T, H, I, E, k, empty):
+    x, W = rnd((T, H), 1), weights(E, H, I)
+    idx, w = routing(T, E, k, empty=empty)
+    w[idx < 0] = float("nan")  # an empty slot's weight is not read into the sum
+    # whatever the workspace held before
+    ws = api.experts_workspace(T, H, I, E, k, "cuda").fill_(0xFF)
+    out = torch.full((T + 1, H), 7.0, dtype=torch.bfloat16, device="cuda")
+    for _ in range(2):
+        api.moe_experts(x, idx, w, *W, out=out[:T], ws=ws)
+        assert api.moe_get_device_status(ws) == api.MOE_OK
+        check(out[:T], x, idx, w, *W)
+        assert bool((out[T] == 7.0).all())
+    gone = (idx < 0).all(1)
+    assert bool((out[:T][gone] == 0).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [20, 400])
+def test_kernel_choices_agree(T):
+    x, W = rnd((T, 256), 1), weights(8, 256, 128)
+    idx, w = routing(T, 8, 4, empty=0.2)
+    ref = api.moe_experts(x, idx, w, *W)
+    check(ref, x, idx, w, *W)
+    try:
+        for name, modes in (("set_layer_gemm", ("always", "never")), ("set_direct_a", ("always", "never")),
+                            ("set_fused_combine", ("always",)), ("set_pair_mma", ("always",))):
+            for m in modes:
+                getattr(api, name)(m)
+                check(api.moe_experts(x, idx, w, *W), x, idx, w, *W)
+                getattr(api, name)("auto")
+    finally:
+        for name in ("set_layer_gemm", "set_direct_a", "set_fused_combine", "set_pair_mma"):
+            getattr(api, name)("auto")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [20, 400])
+def test_indices_outside_are_flagged_and_skipped(T):
+    x, W = rnd((T, 256), 1), weights(8, 256, 128)
+    idx, w = routing(T, 8, 4, empty=0.1)
+    bad = idx.clone()
+    bad[3, 1], bad[7, 0], bad[T - 1, 3] = 8, -2, 2 ** 31 - 1
+    ws = api.experts_workspace(T, 256, 128, 8, 4, "cuda")
+    out = api.moe_experts(x, bad, w, *W, ws=ws)
+    assert api.moe_get_device_status(ws) == 6
+    check(out, x, torch.where((bad < 0) | (bad >= 8), -1, bad), w, *W)
+    api.moe_experts(x, idx, w, *W, ws=ws)
+    assert api.moe_get_device_status(ws) == api.MOE_OK
+
+
+@pytest.mark.gpu
+def test_streams_and_replay():
+    T, H, I, E, k = 100, 256, 128, 16, 4
+    x, W = rnd((T, H), 1), weights(E, H, I)
+    idx, w = routing(T, E, k, empty=0.2)
+    ref = api.moe_experts(x, idx, w, *W)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    outs = [api.moe_experts(x, idx, w, *W, stream=s) for _ in range(3)]
+    s.synchronize()
+    assert all(torch.equal(ref, o) for o in outs)
+    ws = api.experts_workspace(T, H, I, E, k, "cuda")
+    out = torch.empty_like(ref)
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for g in graphs:
+        with torch.cuda.graph(g):
+            api.moe_experts(x, idx, w, *W, out=out, ws=ws)
+    idx.copy_(routing(T, E, k, seed=9, empty=0.5)[0])
+    for g in graphs:
+        out.fill_(3.0)
+        g.replay()
+        torch.cuda.synchronize()
+        check(out, x, idx, w, *W)
+
+
+def quantised(kind, E, H, I):
+    g = torch.Generator(device="cuda").manual_seed(8)
+    byte = lambda *s: torch.randint(0, 256, s, generator=g, device="cuda", dtype=torch.uint8)
+    if kind == "fp8":
+        codes = lambda *s: torch.where((byte(*s) & 0x7F) == 0x7F, 0, byte(*s) & 0xBF)  # |value| < 2, never NaN
+        scale = lambda *s: torch.rand(*s, generator=g, device="cuda") * 0.02 + 0.01
+        return (codes(E, I, H), scale(E, I // 128, H // 128), codes(E, I, H), scale(E, I // 128, H // 128),
+                codes(E, H, I), scale(E, H // 128, I // 128))
+    x8 = lambda *s: torch.full(s, 127 - 6, dtype=torch.uint8, device="cuda")
+    return (byte(E, I, H // 2), x8(E, I, H // 32), byte(E, I, H // 2), x8(E, I, H // 32), byte(E, H, I // 2), x8(E, H, I // 32))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["fp8", "mx"])
+@pytest.mark.parametrize("T", [1, 24, 70, 500])
+def test_quantised_forms_follow_the_routed_forwards(kind, T):
+    H, I, E, k = 512, 512, 8, 2
+    x, W = rnd((T, H), 1), quantised(kind, E, H, I)
+    rw = rnd((H, E), 7, 0.05)
+    idx, w = api.moe_route(x, rw, None, k)
+    ref = getattr(api, f"moe_forward_{kind}")(x, rw, None, *W, k)
+    fn = getattr(api, f"moe_experts_{kind}")
+    out = fn(x, idx, w, *W)
+    assert bool(torch.isfinite(ref.float()).all()) and float(ref.float().abs().max()) > 0
+    assert torch.equal(out, ref)  # the same kernels and sums on the same routing
+    # a slot without an expert is a slot of weight 0
+    gone = torch.rand(T, k, generator=torch.Generator().manual_seed(3)).cuda() < 0.4
+    ws = api.experts_workspace(T, H, I, E, k, "cuda", {"fp8": 1, "mx": 2}[kind]).fill_(0xFF)
+    some = fn(x, torch.where(gone, -1, idx), torch.where(gone, float("nan"), w), *W, ws=ws)
+    assert api.moe_get_device_status(ws) == api.MOE_OK
+    assert torch.equal(some, fn(x, idx, torch.where(gone, 0.0, w), *W))
+    none = fn(x, torch.full_like(idx, -1), w, *W, ws=ws)
+    assert bool((none == 0).all())
+
+
+@pytest.mark.gpu
+def test_python_refusals():
+    x, W = rnd((4, 64), 1), weights(4, 64, 64)
+    idx, w = routing(4, 4, 2)
+    for bad in (lambda: api.moe_experts(x.float(), idx, w, *W), lambda: api.moe_experts(x, idx.long(), w, *W),
+                lambda: api.moe_experts(x, idx, w.bfloat16(), *W), lambda: api.moe_experts(x, idx[:3], w, *W),
+                lambda: api.moe_experts(x, idx, w[:, :1], *W), lambda: api.moe_experts(x, idx, w, W[0], W[1], W[0][:, :32]),
+                lambda: api.moe_experts(x.cpu(), idx, w, *W), lambda: api.moe_experts(x, idx.cpu(), w, *W),
+                lambda: api.moe_experts(x[:, ::2], idx, w, *W)):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(api.MoEError):
+        api.moe_experts(x, idx, w, *W, ws=torch.zeros(1024, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 16, 333])
+def test_a_layer_of_scored_router_experts_and_shared_dense(T):
+    """Router logits, group-limited sigmoid routing, the experts, and a dense gated half added to
+    them, captured as one graph: every stage against 64 bits on the inputs that it had."""
+    from test_linear import check as check_linear
+    from test_route_scored import oracle as route_oracle
+    H, I, E, k, S = 256, 128, 32, 4, 200
+    x, W = rnd((T, H), 1), weights(E, H, I)
+    rw = rnd((E, H), 11, H ** -0.5)
+    bias = rnd((E,), 12, 0.05, torch.float32)
+    sg, su, sd = rnd((S, H), 13, H ** -0.5), rnd((S, H), 14, H ** -0.5), rnd((H, S), 15, S ** -0.5)
+    lws, ews = api.linear_workspace("cuda"), api.experts_workspace(T, H, I, E, k, "cuda")
+
+    def layer():
+        logits = api.moe_linear(x, rw, out_dtype=torch.float32, ws=lws)
+        idx, w = api.moe_route_scored(logits, k, "sigmoid", bias, 8, 3, "top2", True, 2.5)
+        routed = api.moe_experts(x, idx, w, *W, ws=ews)
+        h = api.moe_linear(x, sg, act="silu", w_up=su, ws=lws)
+        return logits, idx, w, routed, h, api.moe_linear(h, sd, residual=routed, ws=lws)
+
+    layer()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = layer()
+    x.copy_(rnd((T, H), 21))
+    graph.replay()
+    torch.cuda.synchronize()
+    logits, idx, w, routed, h, out = got
+    assert torch.equal(logits, check_linear(x, rw, out_dtype=torch.float32))
+    ri, rwt = route_oracle(logits.cpu().numpy(), k, "sigmoid", bias.cpu().numpy(), 8, 3, "top2", True, 2.5)
+    assert np.array_equal(idx.cpu().numpy(), ri) and np.allclose(w.cpu().numpy(), rwt, rtol=1e-5, atol=0)
+    check(routed, x, idx, w, *W)
+    assert torch.equal(h, check_linear(x, sg, act="silu", w_up=su))
+    assert torch.equal(out, check_linear(h, sd, residual=routed))
+    assert api.moe_get_device_status(ews) == api.MOE_OK and api.moe_get_device_status(lws) == api.MOE_OK
+    for a, b in zip(layer(), got):
+        assert torch.equal(a, b)
