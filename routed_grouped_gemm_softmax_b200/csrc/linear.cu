@@ -277,6 +277,16 @@ cudaError_t launch_tile(const moe_linear_t &d, const void *x, const void *w, con
     return w_up ? launch_linear<BN, true>(maps, g, st) : launch_linear<BN, false>(maps, g, st);
 }
 
+cudaError_t launch_pairs(const moe_linear_t &d, const void *x, const void *w, const void *w_up, const LinArgs &g,
+                         cudaStream_t st)
+{
+    LinMaps maps{};
+    if (!encode_rows(&maps.w, w, d.N, d.K, d.ldw, 128) || (w_up && !encode_rows(&maps.w_up, w_up, d.N, d.K, d.ldw, 128)) ||
+        !encode_rows(&maps.x, x, d.M, d.K, d.ldx, 128))
+        return cudaErrorInvalidValue;
+    return launch_linear_pair(maps, g, w_up != nullptr, st);
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -324,7 +334,10 @@ moe_status_t moe_linear(const moe_linear_t *d, const void *x, const void *w, con
     moe::wait_settings(&g.wait_ns, &g.stall_test);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e;
-    if (d->M <= 16)
+    const long long pairs = (long long)((d->M + 255) / 256) * ((d->N + (w_up ? 127 : 255)) / (w_up ? 128 : 256));
+    if (d->M > 128 && pairs * 2 >= moe::num_sms() && (!g.out_f32 || d->K <= 512))
+        e = moe::launch_pairs(*d, x, w, w_up, g, st);
+    else if (d->M <= 16)
         e = moe::launch_tile<16>(*d, x, w, w_up, g, st);
     else if (d->M <= 32)
         e = moe::launch_tile<32>(*d, x, w, w_up, g, st);

@@ -26,6 +26,9 @@ struct LinArgs {
     int mtiles, split, stages;
 };
 
+// linear_pair.cu: 256 x 256 tiles on CTA pairs; maps with boxes of 128 rows.
+cudaError_t launch_linear_pair(const LinMaps &maps, const LinArgs &g, bool gated, cudaStream_t st);
+
 __device__ __forceinline__ void lin_record(int32_t *status) { atomicCAS(status, 0, MOE_ERR_TIMEOUT); }
 
 // act(v).  The forms keep their relative accuracy where v is far below zero: gelu by
