@@ -23,11 +23,22 @@ struct LinArgs {
     int32_t *status;
     uint64_t wait_ns;
     int stall_test;
-    int mtiles, split, stages;
+    bool promote;  // see kPromote
+    // linear_kernel: tiles of x rows, CTAs of a cluster, stages and their 64-column chunks
+    bool gated;
+    int mtiles, split, stages, kc;
 };
 
-// linear_pair.cu: 256 x 256 tiles on CTA pairs; maps with boxes of 128 rows.
-cudaError_t launch_linear_pair(const LinMaps &maps, const LinArgs &g, bool gated, cudaStream_t st);
+// The tensor cores truncate as they accumulate, an error that grows with the depth of the
+// sum: against 64 bits an fp32 result was off by a relative 7e-7 after 1024 columns of K
+// (standard normal operands), where an fp32 chain of rounded sums is at 3e-7.  For fp32 outputs the
+// accumulators are therefore added up outside, with rounding, after every kPromote
+// columns; a bf16 output's own rounding is a thousand times that error.
+constexpr int kPromote = 512;
+
+// linear_pair.cu: 256 x nb tiles (nb 128 or 256) on CTA pairs; maps with boxes of 128 x
+// rows and nb / 2 w rows, two chunks each.
+cudaError_t launch_linear_pair(const LinMaps &maps, const LinArgs &g, bool gated, int nb, cudaStream_t st);
 
 __device__ __forceinline__ void lin_record(int32_t *status) { atomicCAS(status, 0, MOE_ERR_TIMEOUT); }
 
