@@ -174,31 +174,35 @@ def _need_on(t, dev, dtype, shape, name):
 
 def _rows_of(t, dev, dtypes, shape, name) -> int:
     """The row stride, in elements, of a matrix of this shape whose rows are contiguous."""
-    if t.dtype not in dtypes or t.shape != shape or t.device != dev or (t.stride(1) != 1 and shape[1] > 1):
-        raise ValueError(f"{name}: expected {' or '.join(map(str, dtypes))} {tuple(shape)} with contiguous rows on "
-                         f"{dev}, got {t.dtype} {tuple(t.shape)}, strides {t.stride()}, on {t.device}")
-    return t.stride(0) if shape[0] > 1 else max(t.stride(0), shape[1])
+    if t.dtype in dtypes and t.shape == shape and t.device == dev:
+        ld, step = t.stride()
+        if step == 1 or shape[1] <= 1:
+            return ld if shape[0] > 1 else max(ld, shape[1])
+    raise ValueError(f"{name}: expected {' or '.join(map(str, dtypes))} {tuple(shape)} with contiguous rows on "
+                     f"{dev}, got {t.dtype} {tuple(t.shape)}, strides {t.stride()}, on {t.device}")
 
 
-def _empty(shape, dtype, dev, stream):
-    """A new tensor that belongs to the stream the call runs on."""
+def _empty(shape, dtype, like, stream):
+    """A new tensor on the device of `like` that belongs to the stream the call runs on."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return like.new_empty(shape, dtype=dtype)
 
 
 def _call(fn, where, dev, stream, *args):
     """fn(*args, stream) with `dev` current; `stream` (default: dev's current one) must be of `dev`."""
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
+    if stream is None:  # the handle alone: a Stream object would cost 2 us a call
+        handle = torch._C._cuda_getCurrentRawStream(dev.index)
     elif stream.device != dev:
         raise ValueError(f"{where}: a stream of {stream.device} for tensors on {dev}")
+    else:
+        handle = stream.cuda_stream
     if torch.cuda.current_device() == dev.index:
-        code = fn(*args, stream.cuda_stream)
+        code = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
-            code = fn(*args, stream.cuda_stream)
+            code = fn(*args, handle)
     if code != MOE_OK:
         raise MoEError(code, where)
 
@@ -261,11 +265,11 @@ def moe_route_scored(logits, top_k: int, scoring: str = "softmax", bias=None, n_
     if scoring not in SCORINGS or group_score not in GROUP_SCORES:
         raise ValueError(f"scoring {scoring!r} (of {list(SCORINGS)}), group_score {group_score!r} (of {list(GROUP_SCORES)})")
     if topk_idx is None:
-        topk_idx = _empty((T, top_k), torch.int32, dev, stream)
+        topk_idx = _empty((T, top_k), torch.int32, logits, stream)
     else:
         _need_on(topk_idx, dev, torch.int32, (T, top_k), "topk_idx")
     if topk_w is None:
-        topk_w = _empty((T, top_k), torch.float32, dev, stream)
+        topk_w = _empty((T, top_k), torch.float32, logits, stream)
     else:
         _need_on(topk_w, dev, torch.float32, (T, top_k), "topk_w")
     o = Scored(T, E, top_k, SCORINGS[scoring], n_groups, topk_groups, GROUP_SCORES[group_score], bool(renormalize),
@@ -324,7 +328,8 @@ def experts_workspace(T, H, I, E, top_k, device, dtype: int = DTYPE_BF16, stream
     n = int(lib().moe_experts_workspace_size(ctypes.byref(dims(T, H, I, E, top_k)), int(dtype)))
     if n == 0:
         raise MoEError(1, "moe_experts_workspace_size")
-    return _empty(n, torch.uint8, device, stream)
+    with torch.cuda.stream(stream):
+        return torch.empty(n, dtype=torch.uint8, device=device)
 
 
 def _experts(fn, where, dtype, x, topk_idx, topk_w, E, I, weights, out, ws, stream):
@@ -338,7 +343,7 @@ def _experts(fn, where, dtype, x, topk_idx, topk_w, E, I, weights, out, ws, stre
     for t, dt, shape, name in weights:
         _need_on(t, dev, dt, shape, name)
     if out is None:
-        out = _empty((T, H), torch.bfloat16, dev, stream)
+        out = _empty((T, H), torch.bfloat16, x, stream)
     else:
         _need_on(out, dev, torch.bfloat16, (T, H), "out")
     if ws is None:
@@ -463,7 +468,7 @@ def moe_linear(x, w, bias=None, act: str = "none", residual=None, w_up=None, bia
         raise ValueError(f"act {act!r} (of {list(ACTS)}), out_dtype {out_dtype} (bf16 or fp32)")
     ldr = 0 if residual is None else _rows_of(residual, dev, (out_dtype,), (M, N), "residual")
     if out is None:
-        out = _empty((M, N), out_dtype, dev, stream)
+        out = _empty((M, N), out_dtype, x, stream)
     ldo = _rows_of(out, dev, (out_dtype,), (M, N), "out")
     if ws is None:
         ws = linear_workspace(dev, stream)

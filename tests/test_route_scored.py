@@ -193,6 +193,45 @@ def test_extreme_ranges():
     check(x, 8, "sigmoid", inf, 8, 4, "max")
 
 
+def batch64(x, k, scoring, bias, groups, topk_groups, group_score):
+    """The choices and scores of many rows of finite logits, in 64 bits: stable sorts, ties to the lower index."""
+    T, E = x.shape
+    x = x.double()
+    p = torch.sigmoid(x) if scoring == "sigmoid" else torch.softmax(x, 1)
+    c = x if bias is None else p + bias.double()
+    if groups > 1:
+        v = (p if bias is None and group_score == "top2" else c).view(T, groups, E // groups)
+        v = v.sort(dim=2, descending=True).values[:, :, :2 if group_score == "top2" else 1].sum(2)
+        best = v.sort(dim=1, descending=True, stable=True).indices[:, :topk_groups]
+        keep = torch.zeros(T, groups, dtype=torch.bool, device=x.device).scatter_(1, best, True)
+        c = c.masked_fill(~keep.repeat_interleave(E // groups, 1), -math.inf)
+    idx = c.sort(dim=1, descending=True, stable=True).indices[:, :k]
+    return idx, p.gather(1, idx)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,topk_groups,k", [(8, 1, 1, 2), (64, 1, 1, 6), (64, 8, 3, 8), (96, 1, 1, 10), (120, 4, 2, 16),
+                                                    (148, 4, 2, 6), (160, 8, 3, 6), (256, 8, 4, 8), (256, 1, 1, 32), (384, 1, 1, 8), (512, 16, 4, 8),
+                                                    (1000, 1, 1, 8), (1024, 32, 4, 30)])
+def test_every_choice_of_many_rows(scoring, E, groups, topk_groups, k):
+    T = 6001
+    g = torch.Generator().manual_seed(E + k)
+    base = torch.randn(T, E, generator=g)
+    coarse = (torch.randn(E, generator=g) * 4).round() / 64  # biases that repeat
+    for logits in (base, base.bfloat16(), (base * 2).round() / 2, 12 + 3 * base.bfloat16().float(), -9 + 1e-4 * base):
+        x = logits.cuda()
+        for bias in (None, a_bias(E), coarse.cuda(), torch.zeros(E, device="cuda")):
+            for group_score in ("max", "top2") if groups > 1 else ("max",):
+                idx, w = api.moe_route_scored(x, k, scoring, bias, groups, topk_groups, group_score, False)
+                ri, rp = batch64(x.float(), k, scoring, bias, groups, topk_groups, group_score)
+                wrong = (idx != ri).any(1)
+                assert not bool(wrong.any()), (int(wrong.sum()), int(wrong.nonzero()[0]))
+                # exp 4 steps of 2^-24 and its argument's rounding (up to 60 below the maximum here), a sum of at most 37 terms
+                # of such, a quotient and a product
+                assert bool(((w.double() - rp).abs() <= 2.0 ** -24 * (60 + 4 + 60 + 4 + 37 + 4) * rp).all())
+
+
 @pytest.mark.gpu
 def test_given_outputs_streams_and_replay():
     x = rows(300, 256, 4, torch.float32, 11)
