@@ -15,13 +15,15 @@
 // get index -1 and weight 0.
 //
 // Choices are those of 64-bit scores, taken in fp32 wherever that is provably the same.
-// Without a bias experts are ordered by the logits themselves, exactly.  Else fp32 scores
-// carry a bound of their error, and a token is settled by them if every decision of its
-// (each choice against the next, the last one against all that remain, each group
-// kept or dropped) is clear of twice the bound, or is between experts of equal logit
-// and bias, whose scores are equal in any precision.  The few tokens left, and those whose
-// weights leave fp32's range, are done again in 64 bits by one warp each.
-// (16 tokens of 256 experts, sigmoid, bias, groups: 17 us all in 64 bits.)
+// Without a bias experts are ordered by the logits themselves.  Else fp32 scores carry a
+// bound of their error, and a choice stands if it is clear of the next one (the last of all that
+// remain) by twice the bound, or equal to it in logit and bias and so in any precision.  Where
+// not, the experts in question take the place of their 64-bit scores, one a lane; a
+// token whose groups are in question, or whose weights leave fp32's range, is done again with
+// 64-bit scores throughout, and so is a softmax with a bias, for its 64-bit sum.
+// Bound by instructions: about 1100 a warp with bias and groups (256 experts, k 8), 650 a warp of
+// four tokens without (64, k 6).  16 x 256 in 64 bits throughout 17.0 us, so 3.4; 4096 x 256
+// (sigmoid, bias, groups) 31.8 and 8.7; 65536 x 64 bf16 softmax 71.4 and 13.9.
 #include <cfloat>
 #include <climits>
 
@@ -67,7 +69,7 @@ __device__ __forceinline__ Best warp_best(Best b)
 // One token by one warp, every comparison between 64-bit values; lane holds the
 // experts lane, lane + 32, ... (V of them).
 template <int V, typename TL>
-__device__ __noinline__ void route_token_exact(const ScoredArgs &a, const TL *row, int t, int lane)
+__device__ void route_token_exact(const ScoredArgs &a, const TL *row, int t, int lane)
 {
     float l[V];
     double p[V], c[V];
@@ -187,31 +189,50 @@ __global__ void __launch_bounds__(kWarps * 32) route_exact_kernel(const ScoredAr
     route_token_exact<V, TL>(a, static_cast<const TL *>(a.logits) + (size_t)t * a.ld, t, threadIdx.x % 32);
 }
 
-// Floats other than NaN in the order of these keys; 0 is below all of them.
-__device__ __forceinline__ uint32_t key_of(float f)
-{
-    const uint32_t u = __float_as_uint(f + 0.0f);  // -0 and 0 are equal
-    return u ^ (u >> 31 ? 0xffffffffu : 0x80000000u);
-}
-__device__ __forceinline__ float of_key(uint32_t k)
-{
-    return __uint_as_float(k ^ (k >> 31 ? 0x80000000u : 0xffffffffu));
-}
+// Numbers other than NaN in the order of their keys; 0 is below all of them.
+template <typename S>
+struct Keys;
+template <>
+struct Keys<float> {
+    using T = uint32_t;
+    static __device__ __forceinline__ T of(float f)
+    {
+        const T u = __float_as_uint(f + 0.0f);  // -0 and 0 are equal
+        return u ^ (u >> 31 ? 0xffffffffu : 0x80000000u);
+    }
+    static __device__ __forceinline__ float value(T k)
+    {
+        return __uint_as_float(k ^ (k >> 31 ? 0x80000000u : 0xffffffffu));
+    }
+};
+template <>
+struct Keys<double> {
+    using T = unsigned long long;
+    static __device__ __forceinline__ T of(double f)
+    {
+        const T u = static_cast<T>(__double_as_longlong(f + 0.0));
+        return u ^ (u >> 63 ? ~0ull : 1ull << 63);
+    }
+};
 
-// The largest value over the G lanes of a token, on each of them.
-template <int G>
-__device__ __forceinline__ uint32_t group_max(uint32_t v)
+// The largest key over the G lanes of a token, on each of them.
+template <int G, typename K>
+__device__ __forceinline__ K group_max(K v)
 {
-    if constexpr (G == 32) {
+    if constexpr (G == 32 && sizeof(K) == 4) {
         return __reduce_max_sync(kFull, v);
+    } else if constexpr (G == 32) {
+        const uint32_t hi = __reduce_max_sync(kFull, static_cast<uint32_t>(v >> 32));
+        const uint32_t lo = __reduce_max_sync(kFull, v >> 32 == hi ? static_cast<uint32_t>(v) : 0u);
+        return static_cast<K>(hi) << 32 | lo;
     } else {
 #pragma unroll
         for (int o = G / 2; o; o >>= 1) v = max(v, __shfl_xor_sync(kFull, v, o));
         return v;
     }
 }
-template <int G>
-__device__ __forceinline__ float group_sum(float v)
+template <int G, typename S>
+__device__ __forceinline__ S group_sum(S v)
 {
 #pragma unroll
     for (int o = G / 2; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
@@ -243,25 +264,61 @@ __device__ __forceinline__ void load_vec(const __nv_bfloat16 *p, float (&l)[V])
     }
 }
 
-// A token by G lanes, lane s of them the experts s v .. s v + v - 1 (v <= V): a group of experts
-// is a whole number of lanes, equal scores go to the lowest lane.  VE: the experts a lane
-// of route_token_exact holds.
-template <int G, int V, int VE, typename TL>
-__global__ void __launch_bounds__(kWarps * 32) route_scored_kernel(const ScoredArgs a, const int v, const bool vec)
+__device__ __forceinline__ float exp_of(float x) { return expf(x); }
+__device__ __forceinline__ double exp_of(double x) { return exp(x); }
+__device__ __forceinline__ float inverse(float x)
 {
-    pdl_wait();
-    pdl_trigger();
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ double inverse(double x) { return 1.0 / x; }
+
+// Sorts V (a power of two) numbers, the largest first: Batcher's odd-even merges.
+template <int V, typename T>
+__device__ __forceinline__ void sort_down(T (&x)[V])
+{
+#pragma unroll
+    for (int p = 1; p < V; p *= 2)
+#pragma unroll
+        for (int d = p; d >= 1; d /= 2)
+#pragma unroll
+            for (int j = d % p; j + d < V; j += 2 * d)
+#pragma unroll
+                for (int i = j; i < j + d && i + d < V; ++i)
+                    if (i / (2 * p) == (i + d) / (2 * p)) {
+                        const T hi = max(x[i], x[i + d]), lo = min(x[i], x[i + d]);
+                        x[i] = hi, x[i + d] = lo;
+                    }
+}
+
+// How a token's experts lie over its lanes: lane s has the experts s v .. s v + v - 1, so
+// that a group of experts is `span` whole lanes and equal scores go to the lowest lane.
+struct Lanes {
+    int v, span;
+    unsigned per_span;  // lane / span = lane * per_span >> 16
+    bool vec;           // V logits of a lane by 16-byte loads
+};
+
+// Routes a warp's 32 / G tokens from t0 on with scores of type S, those in `wanted` (a
+// mask of their lanes) only.  Writes the tokens whose choices are those of 64 bits and returns
+// a mask of the lanes that found another one (none for S = double).
+template <typename S, int G, int V, typename TL>
+__device__ __forceinline__ unsigned route_tokens(const ScoredArgs &a, const Lanes &at, int t0, unsigned wanted)
+{
+    using K = Keys<S>;
+    constexpr bool kBound = sizeof(S) == 4;  // scores are off by a bounded error
+    // 64 bits: loops rather than straight code, which would be fetched for a token in hundreds
+    constexpr int kUnroll = kBound ? V : 1;
     const int lane = threadIdx.x % 32, sub = lane % G, seg = lane / G;
-    const int t0 = (blockIdx.x * kWarps + threadIdx.x / 32) * (32 / G);
-    if (t0 >= a.T) return;
-    const bool live = t0 + seg < a.T;
-    const int t = live ? t0 + seg : t0;
+    const bool live = wanted >> lane & 1u;
+    const int t = t0 + seg < a.T ? t0 + seg : t0;
     const TL *row = static_cast<const TL *>(a.logits) + (size_t)t * a.ld;
     const bool sigmoid = a.sigmoid, biased = a.bias != nullptr;
-    const int e0 = sub * v;
+    const int e0 = sub * at.v;
 
-    float l[V], b[V], c[V];
-    if (vec) {
+    float l[V], b[V];  // l = -inf: no such expert, or not available
+    if (at.vec) {
         if (e0 < a.E)
             load_vec<V>(row + e0, l);
         else
@@ -269,147 +326,255 @@ __global__ void __launch_bounds__(kWarps * 32) route_scored_kernel(const ScoredA
             for (int i = 0; i < V; ++i) l[i] = -INFINITY;
     } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) l[i] = i < v && e0 + i < a.E ? load_logit(row + e0 + i) : -INFINITY;
+        for (int i = 0; i < V; ++i) l[i] = i < at.v && e0 + i < a.E ? load_logit(row + e0 + i) : -INFINITY;
     }
 #pragma unroll
-    for (int i = 0; i < V; ++i) b[i] = biased && i < v && e0 + i < a.E ? a.bias[e0 + i] : 0.0f;
-    unsigned alive = 0;
+    for (int i = 0; i < V; ++i) l[i] = l[i] > -INFINITY ? fminf(l[i], FLT_MAX) : -INFINITY;  // NaN too
+    if (biased)
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        if (l[i] > -INFINITY && b[i] > -INFINITY) alive |= 1u << i;  // false for NaN
-        l[i] = fminf(l[i], FLT_MAX);
-    }
-
-    float m = 0.0f, inv = 1.0f;
-    if (!sigmoid) {
-        uint32_t mk = 0;
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (alive >> i & 1u) mk = max(mk, key_of(l[i]));
-        mk = group_max<G>(mk);
-        m = mk ? of_key(mk) : 0.0f;
-        float s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (alive >> i & 1u) s += c[i] = expf(l[i] - m);
-        s = group_sum<G>(s);
-        inv = mk ? 1.0f / s : 0.0f;
-    }
-    auto score = [&](float x) { return sigmoid ? __frcp_rn(1.0f + expf(-x)) : expf(x - m) * inv; };
-    // Two scores are in their 64-bit order if they are apart by more than near: each is off by
-    // at most 2^-18 of the largest p (softmax: exp 4 steps of 2^-24 and its argument's
-    // rounding, a sum of V + 5 terms of such, under 64 in all) or by 6 steps of 2^-24 (sigmoid:
-    // exp 4, one sum, one reciprocal); the sum with the bias is rounded once.
-    const float base = (sigmoid ? 0x1p-20f : 0x1p-17f * inv) + 0x1p-120f;
-    bool sure = true;
-    const bool by_p = a.groups > 1 && a.top2 && !biased;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        c[i] = l[i];
-        if (biased || by_p) {
-            const float p = sigmoid ? score(l[i]) : expf(l[i] - m) * inv;
-            c[i] = biased ? p + b[i] : p;
+        for (int i = 0; i < V; ++i) {
+            b[i] = i < at.v && e0 + i < a.E ? a.bias[e0 + i] : 0.0f;
+            l[i] = b[i] > -INFINITY ? l[i] : -INFINITY;
         }
+
+    S m = 0, total = 1, inv = 1;
+    if (!sigmoid) {
+        float most = l[0];
+#pragma unroll
+        for (int i = 1; i < V; ++i) most = fmaxf(most, l[i]);
+        most = Keys<float>::value(group_max<G>(Keys<float>::of(most)));
+        const bool some = most > -INFINITY;
+        m = some ? most : 0.0f;
+        S s = 0;
+#pragma unroll kUnroll
+        for (int i = 0; i < V; ++i) s += exp_of(static_cast<S>(l[i]) - m);
+        s = group_sum<G>(s);
+        if (some) total = s;
+        inv = 1 / total;
+    }
+    // 64 bits: the quotient itself, since sums of scores and biases can tie but for a rounding
+    auto score = [&](float x) {
+        if (sigmoid) return inverse(1 + exp_of(-static_cast<S>(x)));
+        const S e = exp_of(static_cast<S>(x) - m);
+        return kBound ? e * inv : e / total;
+    };
+    // Two fp32 scores are in their 64-bit order if they are apart by more than base: each is off
+    // by at most 2^-18 of the largest p (softmax: exp 4 steps of 2^-24 and its argument's
+    // rounding, a sum of V + 5 terms of such, under 64 in all) or by 7 steps of 2^-24 (sigmoid:
+    // exp 4, one sum, reciprocal 2); and the sum with the bias is rounded once (rel).  Logits
+    // are compared as they are.
+    const float base = static_cast<float>(sigmoid ? 0x1p-20f : 0x1p-17f * inv) + 0x1p-120f;
+    bool sure = true;
+    S c[V];  // what orders the experts
+    if (biased) {
+#pragma unroll kUnroll
+        for (int i = 0; i < V; ++i) c[i] = l[i] > -INFINITY ? score(l[i]) + b[i] : -INFINITY;
+    } else {
+#pragma unroll kUnroll
+        for (int i = 0; i < V; ++i) c[i] = l[i];
     }
 
+    bool dropped = false;
     if (a.groups > 1) {
-        const int span = a.E / a.groups / v;  // lanes of a group
-        const int g = sub / span, in = sub - g * span;
-        float t1 = -INFINITY, t2 = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (alive >> i & 1u) {
-                t2 = fmaxf(t2, fminf(t1, c[i]));
-                t1 = fmaxf(t1, c[i]);
+        const int g = sub * at.per_span >> 16, in = sub - g * at.span;
+        S t1 = -INFINITY, t2 = -INFINITY;
+        if (a.top2 && !biased) {
+#pragma unroll kUnroll
+            for (int i = 0; i < V; ++i) {
+                const S p = l[i] > -INFINITY ? score(l[i]) : -INFINITY;
+                t2 = max(t2, min(t1, p));
+                t1 = max(t1, p);
             }
-        for (int o = 1; o < span; o <<= 1) {  // a group's first lane gathers it
-            const float o1 = __shfl_down_sync(kFull, t1, o, G), o2 = __shfl_down_sync(kFull, t2, o, G);
-            if (in + o < span) {
-                t2 = fmaxf(fminf(t1, o1), fmaxf(t2, o2));
-                t1 = fmaxf(t1, o1);
+        } else {
+#pragma unroll kUnroll
+            for (int i = 0; i < V; ++i) {
+                t2 = max(t2, min(t1, c[i]));
+                t1 = max(t1, c[i]);
+            }
+        }
+        for (int o = 1; o < at.span; o <<= 1) {  // a group's first lane gathers it
+            const S o1 = __shfl_down_sync(kFull, t1, o, G), o2 = __shfl_down_sync(kFull, t2, o, G);
+            if (in + o < at.span) {
+                t2 = max(min(t1, o1), max(t2, o2));
+                t1 = max(t1, o1);
             }
         }
         const bool two = a.top2 && t2 > -INFINITY;
-        float value = two ? t1 + t2 : t1, mag = two ? fabsf(t1) + fabsf(t2) : fabsf(t1);
-        const int from = sub < a.groups ? sub * span : 0;  // lane h takes group h
-        value = __shfl_sync(kFull, value, from, G);
-        mag = __shfl_sync(kFull, mag, from, G);
+        const int from = sub < a.groups ? sub * at.span : 0;  // lane h takes group h
+        S value = __shfl_sync(kFull, two ? t1 + t2 : t1, from, G);
         if (sub >= a.groups) value = -INFINITY;
-        const bool exact = !biased && !a.top2;  // the values are logits
+        const bool bound = kBound && (biased || a.top2);  // else the values are logits
+        float mag = 0.0f;
+        if (bound) mag = __shfl_sync(kFull, static_cast<float>(two ? fabs(t1) + fabs(t2) : fabs(t1)), from, G);
         int above = 0, clear = 0, close = 0;
         for (int h = 0; h < a.groups; ++h) {
-            const float other = __shfl_sync(kFull, value, h, G);
-            const float near = 2.0f * base + 0x1p-22f * (mag + __shfl_sync(kFull, mag, h, G));
+            const S other = __shfl_sync(kFull, value, h, G);
             above += other > value || (other == value && h < sub);
-            clear += other > value + near;                            // above it in any case
-            close += h != sub && other > -INFINITY && !(other < value - near);  // perhaps
-        }
-        const bool keep = value > -INFINITY && above < a.topk_groups;
-        if (!exact && value > -INFINITY) sure = close < a.topk_groups || clear >= a.topk_groups;
-        const unsigned kept = __ballot_sync(kFull, keep) >> (seg * G);
-        if (g >= a.groups || !(kept >> g & 1u)) alive = 0;
-    }
-
-    uint32_t key[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) key[i] = alive >> i & 1u ? key_of(biased ? c[i] : l[i]) : 0;
-
-    // lane j keeps choice j
-    int mine = -1;
-    for (int j = 0; j < a.k; ++j) {
-        uint32_t best = 0;
-#pragma unroll
-        for (int i = 0; i < V; ++i) best = max(best, key[i]);
-        const uint32_t top = group_max<G>(best);
-        const unsigned has = (__ballot_sync(kFull, best == top) >> (seg * G)) & (G == 32 ? kFull : (1u << (G % 32)) - 1u);
-        const int win = __ffs(has) - 1;
-        bool take = sub == win && top != 0;
-        int e = -1;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const bool hit = take && key[i] == top;
-            if (hit) {
-                e = e0 + i;
-                key[i] = 0;
-                take = false;
+            if (bound) {
+                const float near = 2.0f * base + 0x1p-22f * (mag + __shfl_sync(kFull, mag, h, G));
+                clear += other > value + near;                                               // above in any case
+                close += h != sub && other > -INFINITY && !(other < value - near);  // perhaps
             }
         }
-        e = __shfl_sync(kFull, e, win, G);
-        if (sub == j) mine = e;
+        const bool keep = value > -INFINITY && above < a.topk_groups;
+        if (bound && value > -INFINITY) sure = close < a.topk_groups || clear >= a.topk_groups;
+        const unsigned kept = __ballot_sync(kFull, keep) >> (seg * G);
+        dropped = g >= a.groups || !(kept >> g & 1u);
     }
 
-    const bool any = mine >= 0;
-    const float lj = any ? fminf(load_logit(row + mine), FLT_MAX) : 0.0f;
-    const float bj = any && biased ? a.bias[mine] : 0.0f;
-    const float pj = any ? score(lj) : 0.0f;
-    // below fp32's range, but not below that of 64 bits
-    if (any && pj < 1e-30f && lj - m > -750.0f) sure = false;
-    if (biased) {
-        const float cj = pj + bj;
+    // Choices: lane j keeps choice j.  A key at or below that of -inf is none.
+    const typename K::T none = K::of(-INFINITY) | (V - 1);
+    // fp32: the low bits of a key give way to the expert's place in its lane, the lower place
+    // the larger key, so that a lane's keys can be sorted as they are.  Numbers that differ in
+    // those bits alone may come out of order, which the checks below find.
+    typename K::T key[V];
+#pragma unroll kUnroll
+    for (int i = 0; i < V; ++i) {
+        key[i] = dropped ? 0 : K::of(c[i]);
+        if (kBound && !dropped) key[i] = (key[i] & ~static_cast<typename K::T>(V - 1)) | (V - 1 - i);
+    }
+    int mine = -1;
+    // fp32: the best expert left becomes lane j's if its key is at least `from`; a round compares the
+    // lanes' first keys and the winner moves up
+    auto pick = [&](int j, typename K::T from) {
+        const typename K::T first = key[0] & ~static_cast<typename K::T>(V - 1);  // equal ones: the lowest lane's
+        const typename K::T top = group_max<G>(first);
+        unsigned has = __ballot_sync(kFull, first == top);
+        if (G < 32) has = has >> (seg * G) & ((1u << (G % 32)) - 1u);
+        const int win = __ffs(has) - 1;
+        const int e = __shfl_sync(kFull, e0 + V - 1 - static_cast<int>(key[0] & (V - 1)), win, G);
+        const bool ok = (top | (V - 1)) >= from;
+        if (sub == win && ok) {
+#pragma unroll
+            for (int i = 0; i < V - 1; ++i) key[i] = key[i + 1];
+            key[V - 1] = 0;
+        }
+        if (sub == j && ok) mine = e;
+        return ok;
+    };
+    if constexpr (kBound) {
+        sort_down(key);
+        for (int j = 0; j < a.k; ++j) pick(j, none + 1);
+    } else {
+#pragma unroll 1
+        for (int j = 0; j < a.k; ++j) {
+            typename K::T best = 0;
+            int place = 0;
+#pragma unroll 1
+            for (int i = 0; i < V; ++i)
+                if (key[i] > best) {
+                    best = key[i];
+                    place = i;
+                }
+            const typename K::T top = group_max<G>(best);
+            unsigned has = __ballot_sync(kFull, best == top);
+            if (G < 32) has = has >> (seg * G) & ((1u << (G % 32)) - 1u);
+            const int win = __ffs(has) - 1;
+            if (sub == win) key[place] = 0;
+            const int e = __shfl_sync(kFull, e0 + place, win, G);
+            if (sub == j && top > none) mine = e;
+        }
+    }
+
+    float lj = mine >= 0 ? fminf(load_logit(row + mine), FLT_MAX) : 0.0f;
+    float bj = mine >= 0 && biased ? a.bias[mine] : 0.0f;
+    S pj = mine >= 0 ? score(lj) : static_cast<S>(0);
+    int place = sub;  // this lane's choice among the token's
+    const bool whole_keys = sizeof(TL) == 2 && !biased;  // of bf16 logits: what gave way was zero
+    if (kBound && !whole_keys) {
+        // each choice is clear of the next, or equal to it
+        const float cj = biased ? pj + bj : lj, step = biased ? base + 0x1p-22f * fabsf(cj) : 0.0f;
         const float cn = __shfl_down_sync(kFull, cj, 1, G), ln = __shfl_down_sync(kFull, lj, 1, G);
         const float bn = __shfl_down_sync(kFull, bj, 1, G);
         const int next = __shfl_down_sync(kFull, mine, 1, G);
-        if (sub < a.k - 1 && next >= 0 && !(cj - cn > base + 0x1p-22f * fabsf(cj)) && !(lj == ln && bj == bn)) sure = false;
-        const float ck = __shfl_sync(kFull, cj, a.k - 1, G), lk = __shfl_sync(kFull, lj, a.k - 1, G);
-        const float bk = __shfl_sync(kFull, bj, a.k - 1, G);
-        const float floor_k = ck - (base + 0x1p-22f * fabsf(ck));
+        bool settled = !(sub < a.k - 1 && next >= 0 && !(cj - cn > step) && !(lj == ln && bj == bn));
+        // and the experts that are not clearly below the last choice, nor equal to it, are choices
+        const float lk = __shfl_sync(kFull, lj, a.k - 1, G), bk = __shfl_sync(kFull, bj, a.k - 1, G);
+        const float least = __shfl_sync(kFull, cj - step, a.k - 1, G);
+        const bool full = __shfl_sync(kFull, mine, a.k - 1, G) >= 0;
+        int more = mine >= 0 && !(cj < least) && !(lj == lk && bj == bk) ? -1 : 0;
+        if (!dropped)
 #pragma unroll
-        for (int i = 0; i < V; ++i)  // a key is left only where every choice is made
-            if (key[i] && !(of_key(key[i]) < floor_k) && !(l[i] == lk && b[i] == bk)) sure = false;
+            for (int i = 0; i < V; ++i)
+                more += l[i] > -INFINITY && !(c[i] < least) && !(l[i] == lk && (!biased || b[i] == bk));
+#pragma unroll
+        for (int o = G / 2; o; o >>= 1) more += __shfl_xor_sync(kFull, more, o);
+        if (full && more) settled = false;
+        const unsigned doubt = __ballot_sync(kFull, live && !settled);
+        if (doubt) {
+            // All experts that may belong to the choices become candidates, one a lane, and take
+            // the place of their 64-bit score.  A softmax's takes a 64-bit sum: done again below.
+            const unsigned of_seg = G == 32 ? kFull : ((1u << (G % 32)) - 1u) << (seg * G % 32);
+            const bool here = doubt & of_seg;
+            float low = mine >= 0 ? cj - step : INFINITY;
+            const unsigned odd = __ballot_sync(kFull, mine >= 0 && !isfinite(low)) & of_seg;
+#pragma unroll
+            for (int o = G / 2; o; o >>= 1) low = fminf(low, __shfl_xor_sync(kFull, low, o));
+            if (here && (odd || (biased && !sigmoid))) sure = false;
+            bool open = here && full && sure;
+            int n = a.k;
+            while (__any_sync(kFull, open)) {
+                if (n == G) {
+                    if (open) sure = false;
+                    break;
+                }
+                open = pick(n, open ? K::of(low) : 0xffffffffu) && open;
+                ++n;
+            }
+            if (mine >= 0) {
+                lj = fminf(load_logit(row + mine), FLT_MAX);
+                bj = biased ? a.bias[mine] : 0.0f;
+                pj = score(lj);
+            }
+            const double mj = !biased ? lj : 1.0 / (1.0 + exp(-static_cast<double>(lj))) + bj;
+            int before = 0;
+            for (int h = 0; h < n; ++h) {
+                const double mh = __shfl_sync(kFull, mj, h, G);
+                const int eh = __shfl_sync(kFull, mine, h, G);
+                before += eh >= 0 && (mh > mj || (mh == mj && eh < mine));
+            }
+            if (here && mine >= 0) place = before;
+            if (place >= a.k || mine < 0) {
+                pj = 0.0f;
+                if (here && mine >= 0) mine = -2;  // a candidate that is not chosen
+            }
+        }
     }
-    unsigned open = __ballot_sync(kFull, live && !sure);
-    const float sum = group_sum<G>(pj);
+    // below fp32's range, but not below that of 64 bits
+    if (kBound && mine >= 0 && pj < 1e-30f && lj - m > -750.0f) sure = false;
+    const unsigned open = __ballot_sync(kFull, live && !sure);
     const unsigned of_seg = G == 32 ? kFull : ((1u << (G % 32)) - 1u) << (seg * G % 32);
-    if (live && sub < a.k && !(open & of_seg)) {
-        a.idx[(size_t)t * a.k + sub] = mine;
-        const float w = a.renormalize ? (sum > 0.0f ? pj / sum : 0.0f) : pj;
-        a.w[(size_t)t * a.k + sub] = w * a.scale;
+    const S sum = group_sum<G>(pj);
+    if (live && place < a.k && mine > -2 && !(open & of_seg)) {
+        a.idx[(size_t)t * a.k + place] = mine;
+        const S w = a.renormalize ? (sum > 0 ? pj / sum : static_cast<S>(0)) : pj;
+        a.w[(size_t)t * a.k + place] = static_cast<float>(w * a.scale);
     }
-    for (int q = 0; open && q < 32 / G; ++q) {
-        const unsigned of_q = G == 32 ? kFull : ((1u << (G % 32)) - 1u) << (q * G % 32);
-        if (open & of_q)
-            route_token_exact<VE, TL>(a, static_cast<const TL *>(a.logits) + (size_t)(t0 + q) * a.ld, t0 + q, lane);
-    }
+    unsigned again = 0;
+    if (kBound && open)
+        for (int q = 0; q < 32 / G; ++q) {
+            const unsigned of_q = G == 32 ? kFull : ((1u << (G % 32)) - 1u) << (q * G % 32);
+            if (open & of_q) again |= of_q;
+        }
+    return again;
+}
+
+template <int G, int V, typename TL>
+__device__ __noinline__ void route_tokens_64(const ScoredArgs &a, const Lanes &at, int t0, unsigned wanted)
+{
+    route_tokens<double, G, V, TL>(a, at, t0, wanted);
+}
+
+template <int G, int V, typename TL>
+__global__ void __launch_bounds__(kWarps * 32) route_scored_kernel(const ScoredArgs a, const Lanes at)
+{
+    pdl_wait();
+    pdl_trigger();
+    const int t0 = (blockIdx.x * kWarps + threadIdx.x / 32) * (32 / G);
+    if (t0 >= a.T) return;
+    const unsigned here = __ballot_sync(kFull, t0 + (int)(threadIdx.x % 32) / G < a.T);
+    const unsigned again = route_tokens<float, G, V, TL>(a, at, t0, here);
+    if (again) route_tokens_64<G, V, TL>(a, at, t0, again);
 }
 
 // Experts a lane holds when a token has `lanes` of them, V at most: whole lanes a group (0: none).
@@ -422,13 +587,14 @@ int experts_per_lane(const ScoredArgs &a, int lanes, int V)
     return 0;
 }
 
-template <int G, int V, int VE, typename TL>
+template <int G, int V, typename TL>
 cudaError_t launch_lanes(const ScoredArgs &a, int v, cudaStream_t st)
 {
     const int tokens = kWarps * (32 / G), each = 16 / (int)sizeof(TL);
     const bool vec = v == V && a.E % V == 0 && a.ld % each == 0 && reinterpret_cast<uintptr_t>(a.logits) % 16 == 0;
-    return launch_pdl(route_scored_kernel<G, V, VE, TL>, dim3((a.T + tokens - 1) / tokens), dim3(kWarps * 32), 0, st, a,
-                      v, vec);
+    const int span = a.groups > 1 ? a.E / a.groups / v : 32;
+    const Lanes at{v, span, 65536u / span + 1u, vec};
+    return launch_pdl(route_scored_kernel<G, V, TL>, dim3((a.T + tokens - 1) / tokens), dim3(kWarps * 32), 0, st, a, at);
 }
 
 // The fewest lanes a token that hold its experts, eight a lane where that is enough, and its
@@ -436,11 +602,11 @@ cudaError_t launch_lanes(const ScoredArgs &a, int v, cudaStream_t st)
 template <typename TL>
 cudaError_t launch(const ScoredArgs &a, cudaStream_t st)
 {
-    if (int v = experts_per_lane(a, 8, 8)) return launch_lanes<8, 8, 2, TL>(a, v, st);
-    if (int v = experts_per_lane(a, 16, 8)) return launch_lanes<16, 8, 4, TL>(a, v, st);
-    if (int v = experts_per_lane(a, 32, 8)) return launch_lanes<32, 8, 8, TL>(a, v, st);
-    if (int v = experts_per_lane(a, 32, 16)) return launch_lanes<32, 16, 16, TL>(a, v, st);
-    if (int v = experts_per_lane(a, 32, 32)) return launch_lanes<32, 32, 32, TL>(a, v, st);
+    if (int v = experts_per_lane(a, 8, 8)) return launch_lanes<8, 8, TL>(a, v, st);
+    if (int v = experts_per_lane(a, 16, 8)) return launch_lanes<16, 8, TL>(a, v, st);
+    if (int v = experts_per_lane(a, 32, 8)) return launch_lanes<32, 8, TL>(a, v, st);
+    if (int v = experts_per_lane(a, 32, 16)) return launch_lanes<32, 16, TL>(a, v, st);
+    if (int v = experts_per_lane(a, 32, 32)) return launch_lanes<32, 32, TL>(a, v, st);
     const dim3 grid((a.T + kWarps - 1) / kWarps), block(kWarps * 32);
     if (a.E <= 256) return launch_pdl(route_exact_kernel<8, TL>, grid, block, 0, st, a);
     return launch_pdl(route_exact_kernel<32, TL>, grid, block, 0, st, a);
