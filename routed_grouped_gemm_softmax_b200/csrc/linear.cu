@@ -18,8 +18,8 @@
 
 #include "linear.cuh"
 #include "moe_internal.h"
+#include "pair_ptx.cuh"
 #include "pdl.cuh"
-#include "sm100_ptx.cuh"
 
 namespace moe {
 namespace {
@@ -28,7 +28,12 @@ constexpr int LBM = 128;             // w rows per tile
 constexpr int LSTAGES_MAX = 8;
 constexpr int LW_BYTES = LBM * 128;  // one 64-column chunk of 128 w rows
 constexpr int LTHREADS = 192;        // warps 0-3: accumulators; 4: TMA; 5: MMA; all: epilogue
-constexpr int L_HALF_SM = 113 * 1024;  // shared memory of a CTA of which an SM holds two
+constexpr int L_SMEM = 227 * 1024;   // a CTA's shared memory at most
+
+constexpr int LKC = 2;  // 64-column chunks of a stage: 256 contiguous bytes a row
+
+// Rows of a tile that each of `split` CTAs finishes.
+__host__ __device__ __forceinline__ int lin_own(int bn, int split) { return (bn + split - 1) / split; }
 
 struct LinCtrl {
     uint64_t full[LSTAGES_MAX];
@@ -36,6 +41,7 @@ struct LinCtrl {
     uint64_t accf[2];  // accumulator a holds a finished part
     uint64_t acce[2];  // its four warps have read it
     uint64_t fin;      // every MMA of this CTA is done
+    uint64_t red;      // the other CTAs' partials of this one's rows are here
     uint64_t never;    // nothing ever arrives here (timeout test)
     uint32_t tmem_base;
 };
@@ -48,54 +54,52 @@ __device__ __forceinline__ void lin_cluster_wait()
 {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ float4 ld_cluster4(uint32_t addr, uint32_t rank)
+// Copies bytes (a multiple of 16) to the same shared-memory address as dst in CTA `rank` of the
+// cluster, completing on its barrier.
+__device__ __forceinline__ void push_cluster(void *dst, const void *src, uint32_t bytes, uint64_t *bar, uint32_t rank)
 {
-    uint32_t r;
-    float4 v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(r)
-                 : "memory");
-    return v;
+    asm volatile(
+        "{\n\t.reg .b32 d, b;\n\tmapa.shared::cluster.u32 d, %0, %4;\n\tmapa.shared::cluster.u32 b, %3, %4;\n\t"
+        "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [d], [%1], %2, [b];\n\t}" ::"r"(
+            smem_u32(dst)),
+        "r"(smem_u32(src)), "r"(bytes), "r"(smem_u32(bar)), "r"(rank)
+        : "memory");
 }
 
-// Rows rank, rank + S, ... of the tile, each the sum over the cluster's partials.
+// Finishes rows lo .. hi of the tile: four columns a lane, a warp takes one row of 128 columns
+// or two of 64, four times over.  Each is the sum over the cluster's partials in rank order,
+// this CTA's in tile_f and the others' in recv, `recv_rows` rows from each.
 template <int BN, bool GATED>
-__device__ __forceinline__ void finish_rows(const LinArgs &g, const float *tile_f, int nt, int mt, int rank)
+__device__ __forceinline__ void finish_rows(const LinArgs &g, const float *tile_f, const float *recv, int recv_rows,
+                                            int nt, int mt, int lo, int hi, int rank)
 {
-    constexpr int COLS = GATED ? LBM / 2 : LBM, LANES = COLS / 4, RW = 32 / LANES;
+    constexpr int COLS = GATED ? LBM / 2 : LBM, LANES = COLS / 4, RW = 32 / LANES, U = 4;
+    constexpr int STEP = LTHREADS / 32 * RW;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, at = (lane % LANES) * 4;
     const LinCols cols(g, nt * COLS + at);
-    const int rows = min(BN, g.M - mt * BN);
-    const uint32_t base = smem_u32(tile_f);
-    for (int t = rank + g.split * (warp * RW + lane / LANES); t < rows; t += g.split * (LTHREADS / 32) * RW) {
-        float v[4], u[4] = {0.f, 0.f, 0.f, 0.f};
-        if (g.split == 1) {
-            const float4 a = *reinterpret_cast<const float4 *>(tile_f + t * LBM + at);
-            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-            if (GATED) {
-                const float4 b = *reinterpret_cast<const float4 *>(tile_f + t * LBM + COLS + at);
-                u[0] = b.x, u[1] = b.y, u[2] = b.z, u[3] = b.w;
-            }
-        } else {
-            float4 a[8], b[8];  // every rank's loads in flight before the first sum
+#pragma unroll 1
+    for (int t0 = lo + warp * RW + lane / LANES; t0 < hi; t0 += U * STEP) {
+        float v[U][4], u[U][4];
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-                if (q < g.split) {
-                    a[q] = ld_cluster4(base + (t * LBM + at) * 4, q);
-                    if (GATED) b[q] = ld_cluster4(base + (t * LBM + COLS + at) * 4, q);
-                }
-            v[0] = a[0].x, v[1] = a[0].y, v[2] = a[0].z, v[3] = a[0].w;
-            if (GATED) u[0] = b[0].x, u[1] = b[0].y, u[2] = b[0].z, u[3] = b[0].w;
+        for (int j = 0; j < U; ++j)
 #pragma unroll
-            for (int q = 1; q < 8; ++q)
-                if (q < g.split) {
-                    v[0] += a[q].x, v[1] += a[q].y, v[2] += a[q].z, v[3] += a[q].w;
-                    if (GATED) u[0] += b[q].x, u[1] += b[q].y, u[2] += b[q].z, u[3] += b[q].w;
+            for (int i = 0; i < 4; ++i) v[j][i] = u[j][i] = 0.0f;
+#pragma unroll 1
+        for (int q = 0; q < g.split; ++q) {
+            const float *p = q == rank ? tile_f + t0 * LBM + at
+                                       : recv + ((q - (q > rank)) * recv_rows + t0 - lo) * LBM + at;
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+                if (t0 + j * STEP < hi) {
+                    const float4 a = *reinterpret_cast<const float4 *>(p + j * STEP * LBM);
+                    v[j][0] += a.x, v[j][1] += a.y, v[j][2] += a.z, v[j][3] += a.w;
+                    if (GATED) {
+                        const float4 b = *reinterpret_cast<const float4 *>(p + j * STEP * LBM + COLS);
+                        u[j][0] += b.x, u[j][1] += b.y, u[j][2] += b.z, u[j][3] += b.w;
+                    }
                 }
         }
-        lin_finish4<GATED>(g, cols, (int64_t)mt * BN + t, v, u);
+        lin_finish<GATED>(g, cols, (int64_t)mt * BN + t0, STEP, (int64_t)mt * BN + hi, v, u);
     }
 }
 
@@ -104,19 +108,23 @@ __global__ void __launch_bounds__(LTHREADS)
 linear_kernel(const __grid_constant__ LinMaps maps, const LinArgs g)
 {
     constexpr uint32_t ACC = BN < 32 ? 32 : BN;  // TMEM columns of an accumulator
+    constexpr int KC = LKC, STAGE = KC * (LW_BYTES + BN * 128), KSTEP = KC * 64;
     extern __shared__ uint8_t lin_smem[];
     const uint32_t pad = (1024u - (smem_u32(lin_smem) & 1023u)) & 1023u;
     uint8_t *buf = lin_smem + pad;  // stages: w chunks, x chunks
-    const int stage_bytes = g.kc * (LW_BYTES + BN * 128), kstep = g.kc * 64;
-    LinCtrl *S = reinterpret_cast<LinCtrl *>(buf + (size_t)g.stages * stage_bytes);
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    float *recv = reinterpret_cast<float *>(buf + (size_t)g.stages * STAGE);  // the other CTAs' partials of this one's rows
+    LinCtrl *S = reinterpret_cast<LinCtrl *>(recv + (g.split - 1) * lin_own(BN, g.split) * LBM);
+    const int warp = uniform_warp(), lane = threadIdx.x % 32;
     const int rank = blockIdx.x % g.split, tile = blockIdx.x / g.split;
     const int nt = tile / g.mtiles, mt = tile - nt * g.mtiles;
     const int cols_tile = g.gated ? LBM / 2 : LBM;
     // this CTA's K stages, and those of one accumulator
-    const int total = (g.K + kstep - 1) / kstep;
+    const int total = (g.K + KSTEP - 1) / KSTEP;
     const int k0 = (int)((int64_t)total * rank / g.split), k1 = (int)((int64_t)total * (rank + 1) / g.split);
-    const int part = g.promote ? kPromote / kstep : total;
+    const int part = g.promote ? kPromote / KSTEP : total;
+    // CTA q finishes the rows q * own .. of the tile
+    const int rows = min(BN, g.M - mt * BN), own = lin_own(BN, g.split);
+    const int lo = min(rows, rank * own), hi = min(rows, lo + own);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < g.stages; ++s) {
@@ -129,7 +137,9 @@ linear_kernel(const __grid_constant__ LinMaps maps, const LinArgs g)
         }
         mbar_init(&S->fin, 1);
         mbar_init(&S->never, 1);
+        mbar_init(&S->red, 1);
         fence_mbar_init();
+        mbar_arrive_expect_tx(&S->red, (g.split - 1) * (hi - lo) * LBM * 4);
         tma_prefetch_desc(&maps.w);
         if (g.gated) tma_prefetch_desc(&maps.w_up);
         tma_prefetch_desc(&maps.x);
@@ -137,18 +147,25 @@ linear_kernel(const __grid_constant__ LinMaps maps, const LinArgs g)
     if (warp == 5) tmem_alloc(&S->tmem_base, 2 * ACC);
     tc_fence_before();
     __syncthreads();
+    if (g.split > 1) {  // every CTA's barriers exist before a copy may complete on them
+        lin_cluster_arrive();
+        lin_cluster_wait();
+    }
     tc_fence_after();
-    const uint32_t tmem = S->tmem_base;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, S->tmem_base, 0);
     pdl_wait();
     pdl_trigger();
 
-    float sum[BN];  // warps 0-3: lane (of the tile's 128 w rows) x BN rows of x
-#pragma unroll
-    for (int j = 0; j < BN; ++j) sum[j] = 0.0f;
+    float *tile_f = reinterpret_cast<float *>(buf);  // the fp32 tile, [BN rows of x][128 rows of w], in the stages' place
     if (warp < 4) {
+        float sum[BN];  // lane (of the tile's 128 w rows) x BN rows of x
+#pragma unroll
+        for (int j = 0; j < BN; ++j) sum[j] = 0.0f;
+        bool ok = true;
         for (int i = k0, n = 0; i < k1; i += part, ++n) {
             if (!mbar_wait(&S->accf[n & 1], n / 2 & 1, g.wait_ns)) {
                 lin_record(g.status);
+                ok = false;
                 break;
             }
             __syncwarp();
@@ -165,105 +182,123 @@ linear_kernel(const __grid_constant__ LinMaps maps, const LinArgs g)
             __syncwarp();
             if (lane == 0) mbar_arrive(&S->acce[n & 1]);
         }
+        if (ok) {  // every stage was read by an MMA that has completed: its place is free
+#pragma unroll
+            for (int j = 0; j < BN; ++j) tile_f[j * LBM + threadIdx.x] = sum[j];
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     } else if (warp == 4) {
-        if (lane == 0) {
-            int i = 0;
-            for (; i < k1 - k0; ++i) {
-                const int s = i % g.stages;
-                if (!mbar_wait(&S->empty[s], (i / g.stages & 1) ^ 1, g.wait_ns)) {
-                    lin_record(g.status);
-                    break;
-                }
-                uint64_t *bar = &S->full[s];
-                uint8_t *d = buf + (size_t)s * stage_bytes, *dx = d + g.kc * LW_BYTES;
-                const int k = k0 + i;
-                mbar_arrive_expect_tx(bar, stage_bytes);
+        int s = 0, loaded = 0;
+        uint32_t ph = 1;
+        bool ok = true;
+        for (int k = k0; k < k1; ++k, ++loaded) {
+            if (!warp_wait(&S->empty[s], ph, g.wait_ns)) {
+                ok = false;
+                break;
+            }
+            uint64_t *bar = &S->full[s];
+            uint8_t *d = buf + s * STAGE, *dx = d + KC * LW_BYTES;
+            if (elect_one()) {
+                mbar_arrive_expect_tx(bar, STAGE);
                 if (g.chunked) {
                     if (!g.gated) {
-                        tma_load_3d(d, &maps.w, bar, 0, nt * LBM, k * g.kc);
+                        tma_load_3d(d, &maps.w, bar, 0, nt * LBM, k * KC);
                     } else {
-                        for (int c = 0; c < g.kc; ++c) {
-                            tma_load_3d(d + c * LW_BYTES, &maps.w, bar, 0, nt * (LBM / 2), k * g.kc + c);
-                            tma_load_3d(d + c * LW_BYTES + LW_BYTES / 2, &maps.w_up, bar, 0, nt * (LBM / 2),
-                                        k * g.kc + c);
+#pragma unroll
+                        for (int c = 0; c < KC; ++c) {
+                            tma_load_3d(d + c * LW_BYTES, &maps.w, bar, 0, nt * (LBM / 2), k * KC + c);
+                            tma_load_3d(d + c * LW_BYTES + LW_BYTES / 2, &maps.w_up, bar, 0, nt * (LBM / 2), k * KC + c);
                         }
                     }
-                    tma_load_3d(dx, &maps.x, bar, 0, mt * BN, k * g.kc);
+                    tma_load_3d(dx, &maps.x, bar, 0, mt * BN, k * KC);
                 } else {
-                    for (int c = 0; c < g.kc; ++c) {
-                        const int x = k * kstep + c * 64;
+#pragma unroll
+                    for (int c = 0; c < KC; ++c) {
+                        const int x = k * KSTEP + c * 64;
                         tma_load_2d(d + c * LW_BYTES, &maps.w, bar, x, nt * cols_tile);
-                        if (g.gated)
-                            tma_load_2d(d + c * LW_BYTES + LW_BYTES / 2, &maps.w_up, bar, x, nt * cols_tile);
+                        if (g.gated) tma_load_2d(d + c * LW_BYTES + LW_BYTES / 2, &maps.w_up, bar, x, nt * cols_tile);
                         tma_load_2d(dx + c * BN * 128, &maps.x, bar, x, mt * BN);
                     }
                 }
             }
+            __syncwarp();
+            if (++s == g.stages) {
+                s = 0;
+                ph ^= 1;
+            }
+        }
+        if (lane == 0) {
+            if (!ok) lin_record(g.status);
             // never go on with TMA copies still landing in shared memory
-            for (int j = max(0, i - g.stages); j < i; ++j)
+            for (int j = max(0, loaded - g.stages); j < loaded; ++j)
                 if (!mbar_wait(&S->full[j % g.stages], j / g.stages & 1)) lin_record(g.status);
         }
         __syncwarp();
     } else {
-        if (lane == 0) {
-            constexpr uint32_t IDESC = idesc_bf16_f32(LBM, BN);
-            bool ok = !(g.stall_test && !mbar_wait(&S->never, 0, g.wait_ns));
-            for (int i = 0; ok && i < k1 - k0; ++i) {
-                const int s = i % g.stages, n = i / part, in = i % part;
-                if ((in == 0 && !mbar_wait(&S->acce[n & 1], (n / 2 & 1) ^ 1, g.wait_ns)) ||
-                    !mbar_wait(&S->full[s], i / g.stages & 1, g.wait_ns)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t w0 = smem_u32(buf + (size_t)s * stage_bytes), x0 = w0 + g.kc * LW_BYTES;
-                for (int c = 0; c < g.kc; ++c)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_bf16(tmem + (n & 1) * ACC, sw128_kmajor_desc(w0 + c * LW_BYTES + k * 32),
-                                 sw128_kmajor_desc(x0 + c * BN * 128 + k * 32), IDESC, (in | c | k) != 0);
-                mma_commit(&S->empty[s]);
-                if (in == part - 1 || i == k1 - k0 - 1) mma_commit(&S->accf[n & 1]);
+        constexpr uint32_t IDESC = idesc_bf16_f32(LBM, BN);
+        const uint32_t buf0 = smem_u32(buf);
+        bool ok = !(g.stall_test && !warp_wait(&S->never, 0, g.wait_ns));
+        int s = 0, in = 0, n = 0;  // stage, K stage of the accumulator, accumulators begun
+        uint32_t ph = 0;
+        for (int k = k0; ok && k < k1; ++k) {
+            if ((in == 0 && !warp_wait(&S->acce[n & 1], (n / 2 & 1) ^ 1, g.wait_ns)) ||
+                !warp_wait(&S->full[s], ph, g.wait_ns)) {
+                ok = false;
+                break;
             }
-            if (!ok) lin_record(g.status);
-            mma_commit(&S->fin);
-            if (!mbar_wait(&S->fin, 0)) lin_record(g.status);
+            tc_fence_after();
+            const uint32_t w0 = buf0 + s * STAGE, x0 = w0 + KC * LW_BYTES, acc = tmem + (n & 1) * ACC;
+            const bool last = in + 1 == part || k == k1 - 1;
+            if (elect_one()) {
+#pragma unroll
+                for (int c = 0; c < KC; ++c)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        mma_bf16(acc, sw128_kmajor_desc(w0 + c * LW_BYTES + j * 32),
+                                 sw128_kmajor_desc(x0 + c * BN * 128 + j * 32), IDESC, (in | c | j) != 0);
+                mma_commit(&S->empty[s]);
+                if (last) mma_commit(&S->accf[n & 1]);
+            }
+            __syncwarp();
+            if (++s == g.stages) {
+                s = 0;
+                ph ^= 1;
+            }
+            ++in;
+            if (last) {
+                in = 0;
+                ++n;
+            }
         }
+        if (elect_one()) mma_commit(&S->fin);
         __syncwarp();
+        if (!warp_wait(&S->fin, 0)) ok = false;
+        if (!ok && lane == 0) lin_record(g.status);
     }
     tc_fence_before();
-    __syncthreads();  // the stages' shared memory is free
+    __syncthreads();
     if (warp == 5) {
         tc_fence_after();
         tmem_dealloc(tmem, 2 * ACC);
     }
-
-    // the fp32 tile, [BN rows of x][128 rows of w], in the stages' place
-    float *tile_f = reinterpret_cast<float *>(buf);
-    if (warp < 4) {
-#pragma unroll
-        for (int j = 0; j < BN; ++j) tile_f[j * LBM + threadIdx.x] = sum[j];
-    }
     if (g.split > 1) {
-        lin_cluster_arrive();
-        lin_cluster_wait();
-    } else {
-        __syncthreads();
+        if (threadIdx.x < g.split && threadIdx.x != rank) {  // thread q: CTA q's rows of the partial tile
+            const int q = threadIdx.x, qlo = min(rows, q * own), n = min(rows, qlo + own) - qlo;
+            if (n > 0) push_cluster(recv + (rank - (rank > q)) * own * LBM, tile_f + qlo * LBM, n * LBM * 4, &S->red, q);
+        }
+        if (!wait2(&S->red, 0, g.wait_ns)) lin_record(g.status);
+        __syncwarp();
+        lin_cluster_arrive();  // this CTA has what it waits for
     }
-
-    // four columns a lane; a warp takes one row of 128 columns, or two of 64
     if (g.gated)
-        finish_rows<BN, true>(g, tile_f, nt, mt, rank);
+        finish_rows<BN, true>(g, tile_f, recv, own, nt, mt, lo, hi, rank);
     else
-        finish_rows<BN, false>(g, tile_f, nt, mt, rank);
-    if (g.split > 1) {  // leave only when no CTA reads this one's partials any more
-        lin_cluster_arrive();
-        lin_cluster_wait();
-    }
+        finish_rows<BN, false>(g, tile_f, recv, own, nt, mt, lo, hi, rank);
+    if (g.split > 1) lin_cluster_wait();  // leave only when no CTA reads this one's tile any more
 }
 
 // The kernel's limits on the current device: its shared memory limit is raised, and how
-// many clusters of s CTAs of half an SM's shared memory are resident (index s).
+// many clusters of s CTAs, one an SM, are resident (index s).
 template <int BN>
 cudaError_t linear_ready(int (&resident)[9])
 {
@@ -276,7 +311,7 @@ cudaError_t linear_ready(int (&resident)[9])
     if (dev >= 64) return cudaErrorInvalidDevice;
     std::lock_guard<std::mutex> lk(mu);
     if (!(done >> dev & 1ull)) {
-        e = cudaFuncSetAttribute(linear_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+        e = cudaFuncSetAttribute(linear_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, L_SMEM);
         for (int s = 1; e == cudaSuccess && s <= 8; ++s) {
             cudaLaunchAttribute attr[1];
             attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -285,7 +320,7 @@ cudaError_t linear_ready(int (&resident)[9])
             cudaLaunchConfig_t cfg{};
             cfg.gridDim = dim3(s);
             cfg.blockDim = dim3(LTHREADS);
-            cfg.dynamicSmemBytes = L_HALF_SM;
+            cfg.dynamicSmemBytes = L_SMEM;
             cfg.attrs = attr;
             cfg.numAttrs = 1;
             e = cudaOccupancyMaxActiveClusters(&known[dev][s], linear_kernel<BN>, &cfg);
@@ -329,23 +364,23 @@ cudaError_t launch_split(const moe_linear_t &d, const void *x, const void *w, co
     int resident[9];
     cudaError_t e = linear_ready<BN>(resident);
     if (e != cudaSuccess) return e;
-    g.kc = BN <= 64 ? 2 : 1;
+    constexpr int KC = LKC, stage = KC * (LW_BYTES + BN * 128);
     LinMaps maps{};
     // gated stages interleave the chunks of w and w_up, so their boxes hold one chunk
-    if (!encode_operands(&maps, d, x, w, w_up, BN, g.gated ? LBM / 2 : LBM, g.kc, g.gated ? 1 : g.kc))
+    if (!encode_operands(&maps, d, x, w, w_up, BN, g.gated ? LBM / 2 : LBM, KC, g.gated ? 1 : KC))
         return cudaErrorInvalidValue;
-    const int stage = g.kc * (LW_BYTES + BN * 128), cols = g.gated ? LBM / 2 : LBM;
+    const int cols = g.gated ? LBM / 2 : LBM;
     g.mtiles = (g.M + BN - 1) / BN;
     const long long tiles = (long long)((g.N + cols - 1) / cols) * g.mtiles;
-    const int total = (g.K + g.kc * 64 - 1) / (g.kc * 64);
+    const int total = (g.K + KC * 64 - 1) / (KC * 64);
     // as many CTAs as are resident at once, each with a K stage at least
     g.split = 1;
     for (int s = 2; s <= 8 && s <= total; ++s)
         if (tiles <= resident[s]) g.split = s;
     const int own = (total + g.split - 1) / g.split;
-    const int room = g.split <= 2 && tiles * g.split <= num_sms() ? 227 * 1024 : L_HALF_SM;
+    const int recv = (g.split - 1) * lin_own(BN, g.split) * LBM * 4;
     const int need = (BN * LBM * 4 + stage - 1) / stage;  // stages that hold the fp32 tile
-    g.stages = (room - 1024 - (int)sizeof(LinCtrl)) / stage;
+    g.stages = (L_SMEM - 1024 - (int)sizeof(LinCtrl) - recv) / stage;
     if (g.stages > own) g.stages = own;
     if (g.stages > LSTAGES_MAX) g.stages = LSTAGES_MAX;
     if (g.stages < need) g.stages = need;
@@ -358,7 +393,7 @@ cudaError_t launch_split(const moe_linear_t &d, const void *x, const void *w, co
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(tiles * g.split));
     cfg.blockDim = dim3(LTHREADS);
-    cfg.dynamicSmemBytes = 1024 + (size_t)g.stages * stage + sizeof(LinCtrl);
+    cfg.dynamicSmemBytes = 1024 + (size_t)g.stages * stage + recv + sizeof(LinCtrl);
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = g.split > 1 ? 2 : 1;
@@ -393,8 +428,7 @@ cudaError_t launch_linear(const moe_linear_t &d, const void *x, const void *w, c
     }
     if (d.M <= 16) return launch_split<16>(d, x, w, w_up, g, st);
     if (d.M <= 32) return launch_split<32>(d, x, w, w_up, g, st);
-    if (d.M <= 64) return launch_split<64>(d, x, w, w_up, g, st);
-    return launch_split<128>(d, x, w, w_up, g, st);
+    return launch_split<64>(d, x, w, w_up, g, st);
 }
 
 }  // namespace

@@ -24,9 +24,9 @@ struct LinArgs {
     uint64_t wait_ns;
     int stall_test;
     bool promote;  // see kPromote
-    // linear_kernel: tiles of x rows, CTAs of a cluster, stages and their 64-column chunks
+    // linear_kernel: tiles of x rows, CTAs of a cluster, stages
     bool gated;
-    int mtiles, split, stages, kc;
+    int mtiles, split, stages;
 };
 
 // The tensor cores truncate as they accumulate, an error that grows with the depth of the
@@ -57,27 +57,23 @@ __device__ __forceinline__ float lin_act(float v)
     return v;
 }
 
-// act of n values; the activation is the same for the whole launch, so the branch is uniform.
-template <int N>
-__device__ __forceinline__ void lin_act_n(int act, float (&v)[N])
+// act of U x 4 values; the activation is the same for the whole launch, so the branch is uniform.
+template <int ACT, int U>
+__device__ __forceinline__ void lin_act_each(float (&v)[U][4])
+{
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[j][i] = lin_act<ACT>(v[j][i]);
+}
+template <int U>
+__device__ __forceinline__ void lin_act_all(int act, float (&v)[U][4])
 {
     switch (act) {
-    case MOE_ACT_RELU:
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = lin_act<MOE_ACT_RELU>(v[i]);
-        break;
-    case MOE_ACT_GELU:
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = lin_act<MOE_ACT_GELU>(v[i]);
-        break;
-    case MOE_ACT_GELU_TANH:
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = lin_act<MOE_ACT_GELU_TANH>(v[i]);
-        break;
-    case MOE_ACT_SILU:
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = lin_act<MOE_ACT_SILU>(v[i]);
-        break;
+    case MOE_ACT_RELU: lin_act_each<MOE_ACT_RELU>(v); break;
+    case MOE_ACT_GELU: lin_act_each<MOE_ACT_GELU>(v); break;
+    case MOE_ACT_GELU_TANH: lin_act_each<MOE_ACT_GELU_TANH>(v); break;
+    case MOE_ACT_SILU: lin_act_each<MOE_ACT_SILU>(v); break;
     default: break;
     }
 }
@@ -96,67 +92,103 @@ struct LinCols {
     }
 };
 
-// Finishes and stores the four columns of row m: v the products with w, u those with w_up.
-template <bool GATED>
-__device__ __forceinline__ void lin_finish4(const LinArgs &g, const LinCols &c, int64_t m, float (&v)[4],
-                                            const float (&u)[4])
+// Finishes and stores the four columns of the rows m + j * dm below `end`, U of them at once: v
+// the products with w, u those with w_up.  A short batch's epilogue is one pass through this
+// code, so every load is under way before the first is used and there is one branch a
+// choice, not one a row.
+template <bool GATED, int U>
+__device__ __forceinline__ void lin_finish(const LinArgs &g, const LinCols &c, int64_t m, int dm, int64_t end,
+                                           float (&v)[U][4], const float (&u)[U][4])
 {
     if (c.count <= 0) return;
-    const int64_t ro = m * g.ldr + c.n, oo = m * g.ldo + c.n;
     const bool vec = g.vec && c.count == 4;
-    float r[4] = {0.f, 0.f, 0.f, 0.f};
+    float r[U][4];
     if (g.res) {
+        const int64_t at = m * g.ldr + c.n, step = dm * g.ldr;
         if (g.out_f32) {
-            const float *p = static_cast<const float *>(g.res) + ro;
+            const float *p = static_cast<const float *>(g.res) + at;
             if (vec) {
-                const float4 q = *reinterpret_cast<const float4 *>(p);
-                r[0] = q.x, r[1] = q.y, r[2] = q.z, r[3] = q.w;
+#pragma unroll
+                for (int j = 0; j < U; ++j)
+                    if (m + j * dm < end) {
+                        const float4 q = *reinterpret_cast<const float4 *>(p + j * step);
+                        r[j][0] = q.x, r[j][1] = q.y, r[j][2] = q.z, r[j][3] = q.w;
+                    }
             } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (i < c.count) r[i] = p[i];
+                for (int j = 0; j < U; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (i < c.count && m + j * dm < end) r[j][i] = p[j * step + i];
             }
         } else {
-            const __nv_bfloat16 *p = static_cast<const __nv_bfloat16 *>(g.res) + ro;
+            const __nv_bfloat16 *p = static_cast<const __nv_bfloat16 *>(g.res) + at;
             if (vec) {
-                const uint2 q = *reinterpret_cast<const uint2 *>(p);
-                const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&q.x));
-                const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&q.y));
-                r[0] = a.x, r[1] = a.y, r[2] = b.x, r[3] = b.y;
+#pragma unroll
+                for (int j = 0; j < U; ++j)
+                    if (m + j * dm < end) {
+                        const uint2 q = *reinterpret_cast<const uint2 *>(p + j * step);
+                        const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&q.x));
+                        const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&q.y));
+                        r[j][0] = a.x, r[j][1] = a.y, r[j][2] = b.x, r[j][3] = b.y;
+                    }
             } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (i < c.count) r[i] = __bfloat162float(p[i]);
+                for (int j = 0; j < U; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (i < c.count && m + j * dm < end) r[j][i] = __bfloat162float(p[j * step + i]);
             }
         }
     }
+    if (g.bias)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] += c.b[i];
-    lin_act_n(g.act, v);
+        for (int j = 0; j < U; ++j)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (GATED) v[i] *= u[i] + c.bu[i];
-        if (g.res) v[i] += r[i];
-    }
+            for (int i = 0; i < 4; ++i) v[j][i] += c.b[i];
+    lin_act_all(g.act, v);
+    if (GATED)
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[j][i] *= u[j][i] + c.bu[i];
+    if (g.res)
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[j][i] += r[j][i];
+    const int64_t at = m * g.ldo + c.n, step = dm * g.ldo;
     if (g.out_f32) {
-        float *p = static_cast<float *>(g.out) + oo;
+        float *p = static_cast<float *>(g.out) + at;
         if (vec) {
-            *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+                if (m + j * dm < end)
+                    *reinterpret_cast<float4 *>(p + j * step) = make_float4(v[j][0], v[j][1], v[j][2], v[j][3]);
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (i < c.count) p[i] = v[i];
+            for (int j = 0; j < U; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (i < c.count && m + j * dm < end) p[j * step + i] = v[j][i];
         }
     } else {
-        __nv_bfloat16 *p = static_cast<__nv_bfloat16 *>(g.out) + oo;
+        __nv_bfloat16 *p = static_cast<__nv_bfloat16 *>(g.out) + at;
         if (vec) {
-            const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
-            *reinterpret_cast<uint2 *>(p) =
-                make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+                if (m + j * dm < end) {
+                    const __nv_bfloat162 a = __floats2bfloat162_rn(v[j][0], v[j][1]);
+                    const __nv_bfloat162 b = __floats2bfloat162_rn(v[j][2], v[j][3]);
+                    *reinterpret_cast<uint2 *>(p + j * step) =
+                        make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+                }
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (i < c.count) p[i] = __float2bfloat16_rn(v[i]);
+            for (int j = 0; j < U; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (i < c.count && m + j * dm < end) p[j * step + i] = __float2bfloat16_rn(v[j][i]);
         }
     }
 }

@@ -81,7 +81,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
     uint8_t *buf = pair_smem + pad;  // stages: x chunks, w chunks
     float *turn = reinterpret_cast<float *>(buf + PST * P_STAGE);
     PairCtrl *S = reinterpret_cast<PairCtrl *>(turn + P_EPI_WARPS * P_TURN);
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = uniform_warp(), lane = threadIdx.x % 32;
     const uint32_t rank = cluster_rank();
     const int mtiles = (g.M + 255) / 256, ntiles = (g.N + BNO - 1) / BNO;
     const int tiles = mtiles * ntiles, step = gridDim.x / 2, first = blockIdx.x / 2;
@@ -109,27 +109,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
     __syncthreads();
     cluster_sync();  // both CTAs' barriers exist before any remote arrive
     tc_fence_after();
-    const uint32_t tmem = S->tmem_base;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, S->tmem_base, 0);
     pdl_wait();
     pdl_trigger();
 
     if (warp == 0) {
-        if (lane == 0) {
-            const CUtensorMap *wm = GATED && rank == 1 ? &maps.w_up : &maps.w;
-            int issued = 0;
-            bool ok = true;
-            for (int i = first; ok && i < tiles; i += step) {
-                const PairTile t = pair_tile(i, mtiles, ntiles);
-                const int xr = t.mt * 256 + (int)rank * 128;
-                const int wr = t.nt * BNO + (GATED ? 0 : (int)rank * (NB / 2));
-                for (int k = 0; k < kstages; ++k, ++issued) {
-                    const int s = issued % PST;
-                    if (!wait2(&S->empty[s], (issued / PST & 1) ^ 1, g.wait_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t fb = peer_addr(&S->full[s], 0);
-                    uint8_t *d = buf + s * P_STAGE;
+        const CUtensorMap *wm = GATED && rank == 1 ? &maps.w_up : &maps.w;
+        int s = 0, issued = 0;
+        uint32_t ph = 1;
+        bool ok = true;
+        for (int i = first; ok && i < tiles; i += step) {
+            const PairTile t = pair_tile(i, mtiles, ntiles);
+            const int xr = t.mt * 256 + (int)rank * 128;
+            const int wr = t.nt * BNO + (GATED ? 0 : (int)rank * (NB / 2));
+            for (int k = 0; k < kstages; ++k, ++issued) {
+                if (!warp_wait2(&S->empty[s], ph, g.wait_ns)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t fb = peer_addr(&S->full[s], 0);
+                uint8_t *d = buf + s * P_STAGE;
+                if (elect_one()) {
                     if (rank == 0)
                         mbar_arrive_expect_tx(&S->full[s], P_STAGE);
                     else
@@ -138,13 +138,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
                         tma_load_3d_pair(d, &maps.x, fb, 0, xr, 2 * k);
                         tma_load_3d_pair(d + 2 * P_SUB, wm, fb, 0, wr, 2 * k);
                     } else {
+#pragma unroll
                         for (int c = 0; c < 2; ++c) {
                             tma_load_2d_pair(d + c * P_SUB, &maps.x, fb, k * 128 + c * 64, xr);
                             tma_load_2d_pair(d + 2 * P_SUB + c * W_SUB, wm, fb, k * 128 + c * 64, wr);
                         }
                     }
                 }
+                __syncwarp();
+                if (++s == PST) {
+                    s = 0;
+                    ph ^= 1;
+                }
             }
+        }
+        if (lane == 0) {
             if (!ok) lin_record(g.status);
             if (rank == 0)  // never leave with either CTA's copies still landing
                 for (int j = max(0, issued - PST); j < issued; ++j)
@@ -152,37 +160,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
             constexpr uint32_t IDESC = idesc_bf16_f32(256, NB);
-            int used = 0, n = 0;
-            bool ok = !(g.stall_test && !wait2(&S->never, 0, g.wait_ns));
+            const uint32_t buf0 = smem_u32(buf);
+            int s = 0, n = 0;
+            uint32_t ph = 0;
+            bool ok = !(g.stall_test && !warp_wait2(&S->never, 0, g.wait_ns));
             for (int i = first; ok && i < tiles; i += step)
                 for (int k0 = 0; ok && k0 < kstages; k0 += part, ++n) {
                     const int a = n & 1;
-                    if (!wait2(&S->acce[a], (n / 2 & 1) ^ 1, g.wait_ns)) {
+                    if (!warp_wait2(&S->acce[a], (n / 2 & 1) ^ 1, g.wait_ns)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    for (int k = k0; k < min(kstages, k0 + part); ++k, ++used) {
-                        const int s = used % PST;
-                        if (!wait2(&S->full[s], used / PST & 1, g.wait_ns)) {
+                    const int k1 = min(kstages, k0 + part);
+                    for (int k = k0; k < k1; ++k) {
+                        if (!warp_wait2(&S->full[s], ph, g.wait_ns)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
-                        const uint32_t x0 = smem_u32(buf + s * P_STAGE), w0 = x0 + 2 * P_SUB;
+                        const uint32_t x0 = buf0 + s * P_STAGE, w0 = x0 + 2 * P_SUB;
+                        if (elect_one()) {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            mma_bf16_pair(tmem + a * NB, sw128_kmajor_desc(x0 + (j >> 2) * P_SUB + (j & 3) * 32),
-                                          sw128_kmajor_desc(w0 + (j >> 2) * W_SUB + (j & 3) * 32), IDESC,
-                                          (k - k0 | j) != 0);
-                        mma_commit_pair(&S->empty[s]);
+                            for (int j = 0; j < 8; ++j)
+                                mma_bf16_pair(tmem + a * NB, sw128_kmajor_desc(x0 + (j >> 2) * P_SUB + (j & 3) * 32),
+                                              sw128_kmajor_desc(w0 + (j >> 2) * W_SUB + (j & 3) * 32), IDESC,
+                                              (k - k0 | j) != 0);
+                            mma_commit_pair(&S->empty[s]);
+                            if (k == k1 - 1) mma_commit_pair(&S->accf[a]);
+                        }
+                        __syncwarp();
+                        if (++s == PST) {
+                            s = 0;
+                            ph ^= 1;
+                        }
                     }
-                    if (ok) mma_commit_pair(&S->accf[a]);
                 }
-            if (!ok) lin_record(g.status);
-            mma_commit_pair(&S->fin);  // once every MMA issued here has completed
+            if (!ok && lane == 0) lin_record(g.status);
+            if (elect_one()) mma_commit_pair(&S->fin);  // once every MMA issued here has completed
         }
         __syncwarp();
     } else {
@@ -220,27 +237,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
                 *reinterpret_cast<uint4 *>(my + lane * 32 + ((p ^ (lane & 7)) * 4)) =
                     make_uint4(r[4 * p], r[4 * p + 1], r[4 * p + 2], r[4 * p + 3]);
             __syncwarp();
-            if (GATED) {
-                const LinCols cols(g, t.nt * BNO + half * (NB / 4) + c * 16 + (lane & 3) * 4);
+            // lane l: four columns of row r0 + it * RW; the residual of four rows at a time is in flight
+            constexpr int RW = GATED ? 8 : 4;
+            const int p = GATED ? lane & 3 : lane & 7;
+            const int r0 = GATED ? lane / 8 + (lane >> 2 & 1) * 4 : lane / 8;
+            const LinCols cols(g, t.nt * BNO + half * (BNO / 2) + c * (GATED ? 16 : 32) + p * 4);
 #pragma unroll 1
-                for (int it = 0; it < 4; ++it) {
-                    const int rr = it * 8 + lane / 8 + (lane >> 2 & 1) * 4, p = lane & 3;
-                    const float4 v = *reinterpret_cast<const float4 *>(my + rr * 32 + ((p ^ (rr & 7)) * 4));
-                    const float4 u = *reinterpret_cast<const float4 *>(my + rr * 32 + (((p + 4) ^ (rr & 7)) * 4));
-                    float o[4] = {v.x, v.y, v.z, v.w};
-                    const float up[4] = {u.x, u.y, u.z, u.w};
-                    if (row0 + rr < g.M) lin_finish4<true>(g, cols, row0 + rr, o, up);
+            for (int it = 0; it < 32 / RW; it += 4) {
+                float v[4][4], u[4][4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int rr = r0 + (it + j) * RW;
+                    const float4 a = *reinterpret_cast<const float4 *>(my + rr * 32 + ((p ^ (rr & 7)) * 4));
+                    v[j][0] = a.x, v[j][1] = a.y, v[j][2] = a.z, v[j][3] = a.w;
+                    if (GATED) {
+                        const float4 b = *reinterpret_cast<const float4 *>(my + rr * 32 + (((p + 4) ^ (rr & 7)) * 4));
+                        u[j][0] = b.x, u[j][1] = b.y, u[j][2] = b.z, u[j][3] = b.w;
+                    }
                 }
-            } else {
-                const LinCols cols(g, t.nt * BNO + half * (NB / 2) + c * 32 + (lane & 7) * 4);
-#pragma unroll 1
-                for (int it = 0; it < 8; ++it) {
-                    const int rr = it * 4 + lane / 8, p = lane & 7;
-                    const float4 v = *reinterpret_cast<const float4 *>(my + rr * 32 + ((p ^ (rr & 7)) * 4));
-                    float o[4] = {v.x, v.y, v.z, v.w};
-                    const float up[4] = {0.f, 0.f, 0.f, 0.f};
-                    if (row0 + rr < g.M) lin_finish4<false>(g, cols, row0 + rr, o, up);
-                }
+                lin_finish<GATED>(g, cols, row0 + r0 + it * RW, RW, g.M, v, u);
             }
             __syncwarp();
         };

@@ -2,7 +2,7 @@
 // (cta_group::2): peer shared memory and barriers, loads that complete on the leader's
 // barrier, paired TMEM allocation, MMA and commit.
 #pragma once
-#include "sm100_ptx.cuh"
+#include "warp_ptx.cuh"
 
 namespace moe {
 
@@ -93,10 +93,8 @@ __device__ __forceinline__ void mma_bf16_pair(uint32_t d_tmem, uint64_t adesc, u
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, {%5, %6, %7, %8, %9, %10, %11, %12}, p;\n\t}" ::"r"(
-            d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(0u), "r"(0u), "r"(0u), "r"(0u), "r"(0u), "r"(0u),
-        "r"(0u), "r"(0u)
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 // Arrive (once the MMAs issued so far complete) on `bar` in both CTAs of the pair.
@@ -135,4 +133,16 @@ __device__ __forceinline__ bool wait2(uint64_t *bar, uint32_t parity, uint64_t l
     }
 }
 
+// wait2 by a whole converged warp (warp_ptx.cuh).
+__device__ __forceinline__ bool warp_wait2(uint64_t *bar, uint32_t parity, uint64_t limit_ns = kWaitLimitNs)
+{
+    if (__all_sync(0xffffffffu, try_wait_cluster(bar, parity))) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 256; ++i)
+            if (__all_sync(0xffffffffu, try_wait_cluster(bar, parity))) return true;
+        if (__any_sync(0xffffffffu, globaltimer_ns() - t0 > limit_ns)) return false;
+    }
+}
 }  // namespace moe
