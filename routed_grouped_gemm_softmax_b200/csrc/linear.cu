@@ -34,6 +34,11 @@ constexpr int LKC = 2;  // 64-column chunks of a stage: 256 contiguous bytes a r
 
 // Rows of a tile that each of `split` CTAs finishes.
 __host__ __device__ __forceinline__ int lin_own(int bn, int split) { return (bn + split - 1) / split; }
+// Floats of a CTA's buffer for the cluster's partials of its rows.
+__host__ __device__ __forceinline__ int lin_recv(int bn, int split)
+{
+    return split > 1 ? split * lin_own(bn, split) * LBM : 0;
+}
 
 struct LinCtrl {
     uint64_t full[LSTAGES_MAX];
@@ -46,9 +51,11 @@ struct LinCtrl {
     uint32_t tmem_base;
 };
 
+// Relaxed: neither use publishes data (barriers are initialised behind a fence of their own),
+// and a release at cluster scope waits for the thread's earlier memory operations.
 __device__ __forceinline__ void lin_cluster_arrive()
 {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void lin_cluster_wait()
 {
@@ -67,39 +74,52 @@ __device__ __forceinline__ void push_cluster(void *dst, const void *src, uint32_
 }
 
 // Finishes rows lo .. hi of the tile: four columns a lane, a warp takes one row of 128 columns
-// or two of 64, four times over.  Each is the sum over the cluster's partials in rank order,
-// this CTA's in tile_f and the others' in recv, `recv_rows` rows from each.
+// or two of 64, U times over.  Each is the sum, in rank order, over the cluster's partials:
+// `from` holds `stride` rows of each, from row lo on, once `red` completes.  A short
+// batch's epilogue is one pass through this code, most of it latency: the residual and
+// the biases are loaded before the wait, and U is no more than such a batch fills.
 template <int BN, bool GATED>
-__device__ __forceinline__ void finish_rows(const LinArgs &g, const float *tile_f, const float *recv, int recv_rows,
-                                            int nt, int mt, int lo, int hi, int rank)
+__device__ __forceinline__ void finish_rows(const LinArgs &g, const float *from, int stride, uint64_t *red, int nt,
+                                            int mt, int lo, int hi)
 {
-    constexpr int COLS = GATED ? LBM / 2 : LBM, LANES = COLS / 4, RW = 32 / LANES, U = 4;
+    constexpr int COLS = GATED ? LBM / 2 : LBM, LANES = COLS / 4, RW = 32 / LANES, U = BN / 16;
     constexpr int STEP = LTHREADS / 32 * RW;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, at = (lane % LANES) * 4;
     const LinCols cols(g, nt * COLS + at);
+    const int64_t m0 = (int64_t)mt * BN;
+    int t0 = lo + warp * RW + lane / LANES;
+    float r[U][4];
+    lin_residual<U, STEP>(g, cols, m0 + t0, hi - t0, r);
+    if (g.split > 1) {
+        if (!wait2(red, 0, g.wait_ns)) lin_record(g.status);
+        __syncwarp();
+        lin_cluster_arrive();  // this CTA has what it waits for
+    }
 #pragma unroll 1
-    for (int t0 = lo + warp * RW + lane / LANES; t0 < hi; t0 += U * STEP) {
+    while (t0 < hi) {
         float v[U][4], u[U][4];
 #pragma unroll
         for (int j = 0; j < U; ++j)
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[j][i] = u[j][i] = 0.0f;
-#pragma unroll 1
-        for (int q = 0; q < g.split; ++q) {
-            const float *p = q == rank ? tile_f + t0 * LBM + at
-                                       : recv + ((q - (q > rank)) * recv_rows + t0 - lo) * LBM + at;
+        const float *row[U];
 #pragma unroll
-            for (int j = 0; j < U; ++j)
-                if (t0 + j * STEP < hi) {
-                    const float4 a = *reinterpret_cast<const float4 *>(p + j * STEP * LBM);
-                    v[j][0] += a.x, v[j][1] += a.y, v[j][2] += a.z, v[j][3] += a.w;
-                    if (GATED) {
-                        const float4 b = *reinterpret_cast<const float4 *>(p + j * STEP * LBM + COLS);
-                        u[j][0] += b.x, u[j][1] += b.y, u[j][2] += b.z, u[j][3] += b.w;
-                    }
+        for (int j = 0; j < U; ++j) row[j] = from + (min(t0 + j * STEP, hi - 1) - lo) * LBM + at;
+#pragma unroll 2
+        for (int q = 0; q < g.split; ++q)
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                const float *p = row[j] + q * stride * LBM;
+                const float4 a = *reinterpret_cast<const float4 *>(p);
+                v[j][0] += a.x, v[j][1] += a.y, v[j][2] += a.z, v[j][3] += a.w;
+                if (GATED) {
+                    const float4 b = *reinterpret_cast<const float4 *>(p + COLS);
+                    u[j][0] += b.x, u[j][1] += b.y, u[j][2] += b.z, u[j][3] += b.w;
                 }
-        }
-        lin_finish<GATED>(g, cols, (int64_t)mt * BN + t0, STEP, (int64_t)mt * BN + hi, v, u);
+            }
+        lin_finish<GATED, U, STEP>(g, cols, m0 + t0, hi - t0, v, u, r);
+        t0 += U * STEP;
+        if (t0 < hi) lin_residual<U, STEP>(g, cols, m0 + t0, hi - t0, r);
     }
 }
 
@@ -112,8 +132,8 @@ linear_kernel(const __grid_constant__ LinMaps maps, const LinArgs g)
     extern __shared__ uint8_t lin_smem[];
     const uint32_t pad = (1024u - (smem_u32(lin_smem) & 1023u)) & 1023u;
     uint8_t *buf = lin_smem + pad;  // stages: w chunks, x chunks
-    float *recv = reinterpret_cast<float *>(buf + (size_t)g.stages * STAGE);  // the other CTAs' partials of this one's rows
-    LinCtrl *S = reinterpret_cast<LinCtrl *>(recv + (g.split - 1) * lin_own(BN, g.split) * LBM);
+    float *recv = reinterpret_cast<float *>(buf + (size_t)g.stages * STAGE);  // every CTA's partials of this one's rows
+    LinCtrl *S = reinterpret_cast<LinCtrl *>(recv + lin_recv(BN, g.split));
     const int warp = uniform_warp(), lane = threadIdx.x % 32;
     const int rank = blockIdx.x % g.split, tile = blockIdx.x / g.split;
     const int nt = tile / g.mtiles, mt = tile - nt * g.mtiles;
@@ -139,7 +159,7 @@ linear_kernel(const __grid_constant__ LinMaps maps, const LinArgs g)
         mbar_init(&S->never, 1);
         mbar_init(&S->red, 1);
         fence_mbar_init();
-        mbar_arrive_expect_tx(&S->red, (g.split - 1) * (hi - lo) * LBM * 4);
+        mbar_arrive_expect_tx(&S->red, g.split > 1 ? g.split * (hi - lo) * LBM * 4 : 0);
         tma_prefetch_desc(&maps.w);
         if (g.gated) tma_prefetch_desc(&maps.w_up);
         tma_prefetch_desc(&maps.x);
@@ -281,19 +301,16 @@ linear_kernel(const __grid_constant__ LinMaps maps, const LinArgs g)
         tc_fence_after();
         tmem_dealloc(tmem, 2 * ACC);
     }
-    if (g.split > 1) {
-        if (threadIdx.x < g.split && threadIdx.x != rank) {  // thread q: CTA q's rows of the partial tile
-            const int q = threadIdx.x, qlo = min(rows, q * own), n = min(rows, qlo + own) - qlo;
-            if (n > 0) push_cluster(recv + (rank - (rank > q)) * own * LBM, tile_f + qlo * LBM, n * LBM * 4, &S->red, q);
-        }
-        if (!wait2(&S->red, 0, g.wait_ns)) lin_record(g.status);
-        __syncwarp();
-        lin_cluster_arrive();  // this CTA has what it waits for
+    if (threadIdx.x < g.split && g.split > 1) {  // thread q: CTA q's rows of this partial tile
+        const int q = threadIdx.x, qlo = min(rows, q * own), n = min(rows, qlo + own) - qlo;
+        if (n > 0) push_cluster(recv + rank * own * LBM, tile_f + qlo * LBM, n * LBM * 4, &S->red, q);
     }
+    __syncwarp();
+    const float *from = g.split > 1 ? recv : tile_f;
     if (g.gated)
-        finish_rows<BN, true>(g, tile_f, recv, own, nt, mt, lo, hi, rank);
+        finish_rows<BN, true>(g, from, own, &S->red, nt, mt, lo, hi);
     else
-        finish_rows<BN, false>(g, tile_f, recv, own, nt, mt, lo, hi, rank);
+        finish_rows<BN, false>(g, from, own, &S->red, nt, mt, lo, hi);
     if (g.split > 1) lin_cluster_wait();  // leave only when no CTA reads this one's tile any more
 }
 
@@ -378,7 +395,7 @@ cudaError_t launch_split(const moe_linear_t &d, const void *x, const void *w, co
     for (int s = 2; s <= 8 && s <= total; ++s)
         if (tiles <= resident[s]) g.split = s;
     const int own = (total + g.split - 1) / g.split;
-    const int recv = (g.split - 1) * lin_own(BN, g.split) * LBM * 4;
+    const int recv = lin_recv(BN, g.split) * 4;
     const int need = (BN * LBM * 4 + stage - 1) / stage;  // stages that hold the fp32 tile
     g.stages = (L_SMEM - 1024 - (int)sizeof(LinCtrl) - recv) / stage;
     if (g.stages > own) g.stages = own;
@@ -400,11 +417,19 @@ cudaError_t launch_split(const moe_linear_t &d, const void *x, const void *w, co
     return cudaLaunchKernelEx(&cfg, linear_kernel<BN>, maps, g);
 }
 
-cudaError_t launch_pairs(const moe_linear_t &d, const void *x, const void *w, const void *w_up, const LinArgs &g,
-                         int nb, cudaStream_t st)
+cudaError_t launch_pairs(const moe_linear_t &d, const void *x, const void *w, const void *w_up, LinArgs g, int nb,
+                         cudaStream_t st)
 {
     LinMaps maps{};
     if (!encode_operands(&maps, d, x, w, w_up, 128, nb / 2, 2, 2)) return cudaErrorInvalidValue;
+    const int size = g.out_f32 ? 4 : 2;
+    auto mapped = [&](const void *p, int64_t ld) {
+        return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * size % 16 == 0 && ld < (int64_t)1 << 37;
+    };
+    g.maps_out = mapped(g.out, g.ldo) && (!g.res || mapped(g.res, g.ldr));
+    if (g.maps_out && (!encode_rows_32(&maps.out, g.out, g.out_f32, d.M, d.N, g.ldo) ||
+                       (g.res && !encode_rows_32(&maps.res, g.res, g.out_f32, d.M, d.N, g.ldr))))
+        return cudaErrorInvalidValue;
     return launch_linear_pair(maps, g, g.gated, nb, st);
 }
 
@@ -424,7 +449,7 @@ cudaError_t launch_linear(const moe_linear_t &d, const void *x, const void *w, c
     };
     if (d.M > 128 && tiles(128) >= 32) {
         const long long w128 = (tiles(128) + pairs - 1) / pairs, w256 = (tiles(256) + pairs - 1) / pairs;
-        return launch_pairs(d, x, w, w_up, g, 3 * w256 <= 2 * w128 ? 256 : 128, st);
+        return launch_pairs(d, x, w, w_up, g, !g.promote && 3 * w256 <= 2 * w128 ? 256 : 128, st);
     }
     if (d.M <= 16) return launch_split<16>(d, x, w, w_up, g, st);
     if (d.M <= 32) return launch_split<32>(d, x, w, w_up, g, st);

@@ -10,9 +10,12 @@
 // tile run under the next one's products.
 //
 // Warp 0 streams x and w (TMA), warp 1 of CTA 0 issues the MMAs, warps 2-9 finish tiles:
-// each reads its 32 accumulator rows 32 columns at a time, turns them in shared memory so
-// that a row's columns lie in neighbouring lanes, and finishes four columns a lane (one
-// contiguous run of residual and out a row, whatever the rows' alignment).  Tiles are
+// each takes its 32 accumulator rows, a lane each, and half the columns in boxes of 32, applies
+// bias, activation and gate in registers, and stores a box from shared memory by
+// tensor map; the residual's box arrives at the same place before.  (Rows turned in shared
+// memory and stored four columns a lane took 3700 cycles a box's worth, whose latency a tile
+// that is a CTA's last does not hide: 512 x 2048 x 2048 11.6 us.)  Where rows of out or
+// residual are not 16-byte aligned a box is written row by row, a column a lane.  Tiles are
 // dealt out statically, bands of 8 row tiles walked column by column, so that the
 // tiles in flight share x and w rows in L2.  Every wait is bounded.
 #include <mutex>
@@ -29,7 +32,7 @@ constexpr int P_SUB = 128 * 128;        // 128 x rows x 64 columns
 constexpr int P_EPI_WARPS = 8;
 constexpr int P_THREADS = 64 + 32 * P_EPI_WARPS;
 constexpr int P_BAND = 8;               // row tiles of a band
-constexpr int P_TURN = 32 * 32;         // floats of a warp's turning buffer
+constexpr int P_BOX = 4096;             // bytes of a warp's boxes: 32 x 32 fp32, or two of bf16 in turn
 constexpr int PST_MAX = 4;
 
 // Tiles of 256 rows x NB accumulator columns; a CTA's stage: 128 x rows, NB / 2 w rows, 128
@@ -47,14 +50,14 @@ struct PairCtrl {
     uint64_t accf[2];     // each: accumulator a holds a finished tile
     uint64_t acce[2];     // leader: every epilogue warp of the pair drained accumulator a
     uint64_t fin;         // each: every MMA of the pair completed
-    uint64_t bye;         // each: the other CTA is done touching this one
+    uint64_t res[2 * P_EPI_WARPS];  // the residual's box of an epilogue warp is here
     uint64_t never;       // nothing ever arrives here (timeout test)
     uint32_t tmem_base;
 };
 
 template <int NB>
 constexpr size_t kPairSmem =
-    1024 + (size_t)PairShape<NB>::ST * PairShape<NB>::STAGE + P_EPI_WARPS * P_TURN * 4 + sizeof(PairCtrl);
+    1024 + (size_t)PairShape<NB>::ST * PairShape<NB>::STAGE + P_EPI_WARPS * P_BOX + sizeof(PairCtrl);
 static_assert(kPairSmem<256> <= 227 * 1024 && kPairSmem<128> <= 227 * 1024, "one CTA's shared memory");
 
 struct PairTile {
@@ -68,6 +71,264 @@ __device__ __forceinline__ PairTile pair_tile(int i, int mtiles, int ntiles)
     return {band * P_BAND + at % h, at / h};
 }
 
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *tm, const void *src, int x, int y)
+{
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];\n\t"
+                 "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(tm)),
+                 "r"(smem_u32(src)), "r"(x), "r"(y)
+                 : "memory");
+}
+// At most N of this thread's stores still read shared memory.
+template <int N>
+__device__ __forceinline__ void stores_read()
+{
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// Box (row, col) row by row, a column a lane, with plain accesses: fp32 in `from`, 16-byte
+// piece p of row r at p ^ (r % 8).  FULL: all 32 rows are there, none needs a test.
+template <typename T, bool FULL>
+__device__ __forceinline__ void store_rows(const LinArgs &g, const uint8_t *from, int row, int rows, int c, int lane)
+{
+    T *out = static_cast<T *>(g.out) + (int64_t)row * g.ldo + c;
+    const T *res = static_cast<const T *>(g.res) + (int64_t)row * g.ldr + c;
+#pragma unroll 1
+    for (int r0 = 0; r0 < rows; r0 += 16) {
+        T r[16];
+        if (g.res)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (FULL || r0 + i < rows) r[i] = res[(r0 + i) * g.ldr];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float o = *reinterpret_cast<const float *>(from + (r0 + i) * 128 + ((lane / 4) ^ (i & 7)) * 16 + lane % 4 * 4);
+            if (g.res) o += static_cast<float>(r[i]);
+            if (FULL || r0 + i < rows) out[(r0 + i) * g.ldo] = static_cast<T>(o);
+        }
+    }
+}
+
+// An epilogue warp's part of the tiles: rows 32 (ew % 4) .. of the CTA's 128, columns ew / 4 of
+// two halves.
+template <int NB, bool GATED, bool PROMOTE>
+__device__ __forceinline__ void pair_epilogue(const LinMaps &maps, const LinArgs &g, PairCtrl *S, uint8_t *box,
+                                              uint32_t tmem, int ew, int lane, uint32_t rank, int part)
+{
+    constexpr int BNO = GATED ? NB / 2 : NB, BOXES = BNO / 2 / 32;
+    const int warp = ew + 2, q = warp & 3, half = ew / 4;  // a warp reads the TMEM lanes of its quarter
+    const int mtiles = (g.M + 255) / 256, ntiles = (g.N + BNO - 1) / BNO;
+    const int tiles = mtiles * ntiles, step = gridDim.x / 2, first = blockIdx.x / 2;
+    const int kstages = (g.K + 127) / 128;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * (BNO / 2);
+    const bool as_f32 = g.out_f32 || !g.maps_out;  // a box's type
+    const int row_bytes = as_f32 ? 128 : 64, turns = as_f32 ? 1 : 2;
+    const int swizzle = as_f32 ? lane & 7 : lane >> 1 & 3;
+    uint64_t *rbar = &S->res[2 * ew];
+    const bool res_maps = g.res && g.maps_out;
+
+    auto origin = [&](const PairTile &t, int &row, int &col) {
+        row = t.mt * 256 + (int)rank * 128 + q * 32;
+        col = t.nt * BNO + half * (BNO / 2);
+    };
+    auto boxes_of = [&](int row, int col) {  // how many boxes of a tile lie in out, from the first on
+        return row < g.M && col < g.N ? min(BOXES, (g.N - col + 31) / 32) : 0;
+    };
+    int bx = 0, loads = 0;  // boxes begun, residual boxes asked for
+    // the residual's box into place `slot`, once what was stored from there has been read
+    auto load_residual = [&](int slot, int row, int col) {
+        if (lane == 0) {
+            stores_read<0>();
+            mbar_arrive_expect_tx(rbar + slot, 32 * row_bytes);
+            tma_load_2d(box + slot * 2048, &maps.res, rbar + slot, col, row);
+        }
+        ++loads;
+        __syncwarp();
+    };
+    // the residual of the next box after box j of `count` of tile i
+    auto load_next = [&](int i, int j, int count, int row, int col) {
+        if (j + 1 < count) {
+            load_residual(bx & (turns - 1), row, col + (j + 1) * 32);
+            return;
+        }
+        for (i += step; i < tiles; i += step) {
+            origin(pair_tile(i, mtiles, ntiles), row, col);
+            if (boxes_of(row, col)) {
+                load_residual(bx & (turns - 1), row, col);
+                return;
+            }
+        }
+    };
+    auto drained = [&](int a) {  // the accumulator is free for the part after next
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+            if (rank == 0)
+                mbar_arrive(&S->acce[a]);
+            else
+                arrive_remote(peer_addr(&S->acce[a], 0));
+        }
+    };
+    // 16 columns, the part h of a box at `to`: v the products with w, u those with w_up
+    auto finish = [&](float (&v)[4][4], const float (&u)[4][4], uint8_t *to, int h, float bias,
+                      float bias_up) __attribute__((always_inline)) {
+        if (g.bias)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i / 4][i % 4] += __shfl_sync(0xffffffffu, bias, h * 16 + i);
+        lin_act_all(g.act, v);
+        if (GATED)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                v[i / 4][i % 4] *= u[i / 4][i % 4] + __shfl_sync(0xffffffffu, bias_up, h * 16 + i);
+        uint8_t *mine = to + lane * row_bytes;
+        if (as_f32) {
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                float4 *at = reinterpret_cast<float4 *>(mine + ((h * 4 + p) ^ swizzle) * 16);
+                if (res_maps) {
+                    const float4 r = *at;
+                    v[p][0] += r.x, v[p][1] += r.y, v[p][2] += r.z, v[p][3] += r.w;
+                }
+                *at = make_float4(v[p][0], v[p][1], v[p][2], v[p][3]);
+            }
+        } else {
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                uint4 *at = reinterpret_cast<uint4 *>(mine + ((h * 2 + p) ^ swizzle) * 16);
+                uint32_t w[4];
+                if (res_maps) {
+                    const uint4 r = *at;
+                    w[0] = r.x, w[1] = r.y, w[2] = r.z, w[3] = r.w;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float a = v[2 * p + i / 2][i % 2 * 2], b = v[2 * p + i / 2][i % 2 * 2 + 1];
+                    if (res_maps) {
+                        a += __uint_as_float(w[i] << 16);
+                        b += __uint_as_float(w[i] & 0xffff0000u);
+                    }
+                    const __nv_bfloat162 o = __floats2bfloat162_rn(a, b);
+                    w[i] = *reinterpret_cast<const uint32_t *>(&o);
+                }
+                *at = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+    };
+
+    if (res_maps) load_next(first - step, 0, 0, 0, 0);
+    int n = 0;  // accumulators read
+    for (int i = first; i < tiles; i += step) {
+        int row, col;
+        origin(pair_tile(i, mtiles, ntiles), row, col);
+        const int count = boxes_of(row, col);
+        float bias[BOXES], bias_up[BOXES];  // a column a lane
+#pragma unroll
+        for (int j = 0; j < BOXES; ++j) {
+            const int c = col + j * 32 + lane;
+            bias[j] = g.bias && c < g.N ? g.bias[c] : 0.0f;
+            bias_up[j] = GATED && g.bias_up && c < g.N ? g.bias_up[c] : 0.0f;
+        }
+        float sum[PROMOTE ? NB / 2 : 1];
+        uint32_t acc = lanes;
+        if constexpr (PROMOTE) {
+#pragma unroll
+            for (int j = 0; j < NB / 2; ++j) sum[j] = 0.0f;
+        }
+        const int parts = PROMOTE ? (kstages + part - 1) / part : 1;
+        for (int k = 0; k < parts; ++k) {
+            if (!wait2(&S->accf[n & 1], n / 2 & 1, g.wait_ns)) {
+                lin_record(g.status);
+                stores_done();  // never leave with copies still landing
+                if (loads > bx && !mbar_wait(rbar + (bx & (turns - 1)), bx / turns & 1)) lin_record(g.status);
+                __syncwarp();
+                return;
+            }
+            __syncwarp();
+            tc_fence_after();
+            acc = lanes + (n & 1) * NB;
+            if constexpr (PROMOTE) {
+#pragma unroll
+                for (int c = 0; c < NB / 32; ++c) {
+                    uint32_t r[16];
+                    tmem_ld16_sync(acc + (GATED && c >= NB / 64 ? NB / 2 + (c - NB / 64) * 16 : c * 16), r);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) sum[c * 16 + j] += __uint_as_float(r[j]);
+                }
+                drained(n & 1);
+            } else if (count == 0) {
+                drained(n & 1);
+            }
+            ++n;
+        }
+#pragma unroll(PROMOTE ? BOXES : 1)
+        for (int j = 0; j < BOXES; ++j) {
+            if (j >= count) continue;
+            const int slot = bx & (turns - 1);
+            uint8_t *to = box + slot * 2048;
+            float b = bias[0], bu = bias_up[0];
+#pragma unroll
+            for (int k = 1; k < BOXES; ++k)
+                if (j == k) b = bias[k], bu = bias_up[k];
+            if (res_maps) {
+                if (!mbar_wait(rbar + slot, bx / turns & 1, g.wait_ns)) lin_record(g.status);
+            } else if (g.maps_out && lane == 0) {
+                if (turns == 2)
+                    stores_read<1>();
+                else
+                    stores_read<0>();
+            }
+            __syncwarp();
+            ++bx;
+            if (res_maps && turns == 2) load_next(i, j, count, row, col);
+#pragma unroll(PROMOTE ? 2 : 1)
+            for (int h = 0; h < 2; ++h) {
+                float v[4][4], u[4][4];
+                if constexpr (PROMOTE) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        v[e / 4][e % 4] = sum[(2 * j + h) * 16 + e];
+                        if (GATED) u[e / 4][e % 4] = sum[NB / 4 + (2 * j + h) * 16 + e];
+                    }
+                } else {
+                    uint32_t lo[16], hi[16];
+                    const uint32_t at = acc + (2 * j + h) * 16;
+                    if (GATED)
+                        tmem_ld16x2_sync(at, at + NB / 2, lo, hi);
+                    else
+                        tmem_ld16_sync(at, lo);
+                    if (h == 1 && j == count - 1) drained((n - 1) & 1);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        v[e / 4][e % 4] = __uint_as_float(lo[e]);
+                        if (GATED) u[e / 4][e % 4] = __uint_as_float(hi[e]);
+                    }
+                }
+                finish(v, u, to, h, b, bu);
+            }
+            if (g.maps_out) {
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) tma_store_2d(&maps.out, to, col + j * 32, row);
+                if (res_maps && turns == 1) load_next(i, j, count, row, col);
+            } else {
+                __syncwarp();
+                const int c = col + j * 32 + lane, rows = min(32, g.M - row);
+                if (c < g.N) {
+                    if (g.out_f32) {
+                        rows == 32 ? store_rows<float, true>(g, to, row, rows, c, lane)
+                                   : store_rows<float, false>(g, to, row, rows, c, lane);
+                    } else {
+                        rows == 32 ? store_rows<__nv_bfloat16, true>(g, to, row, rows, c, lane)
+                                   : store_rows<__nv_bfloat16, false>(g, to, row, rows, c, lane);
+                    }
+                }
+            }
+            __syncwarp();
+        }
+    }
+    stores_done();
+}
+
 // PROMOTE: after every 512 columns of K the accumulator is added to fp32 registers of the
 // epilogue warps (see kPromote).
 template <int NB, bool GATED, bool PROMOTE>
@@ -79,8 +340,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
     extern __shared__ uint8_t pair_smem[];
     const uint32_t pad = (1024u - (smem_u32(pair_smem) & 1023u)) & 1023u;
     uint8_t *buf = pair_smem + pad;  // stages: x chunks, w chunks
-    float *turn = reinterpret_cast<float *>(buf + PST * P_STAGE);
-    PairCtrl *S = reinterpret_cast<PairCtrl *>(turn + P_EPI_WARPS * P_TURN);
+    uint8_t *boxes = buf + PST * P_STAGE;
+    PairCtrl *S = reinterpret_cast<PairCtrl *>(boxes + P_EPI_WARPS * P_BOX);
     const int warp = uniform_warp(), lane = threadIdx.x % 32;
     const uint32_t rank = cluster_rank();
     const int mtiles = (g.M + 255) / 256, ntiles = (g.N + BNO - 1) / BNO;
@@ -98,11 +359,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
             mbar_init(&S->acce[a], 2 * P_EPI_WARPS);
         }
         mbar_init(&S->fin, 1);
-        mbar_init(&S->bye, 1);
+        for (int i = 0; i < 2 * P_EPI_WARPS; ++i) mbar_init(&S->res[i], 1);
         mbar_init(&S->never, 1);
         fence_mbar_init();
         tma_prefetch_desc(&maps.x);
         tma_prefetch_desc(GATED && rank == 1 ? &maps.w_up : &maps.w);
+        if (g.maps_out) tma_prefetch_desc(&maps.out);
+        if (g.maps_out && g.res) tma_prefetch_desc(&maps.res);
     }
     if (warp == 1) tmem_alloc_pair(&S->tmem_base, 2 * NB);
     tc_fence_before();
@@ -203,114 +466,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
         }
         __syncwarp();
     } else {
-        const int q = warp & 3, half = (warp - 2) / 4;
-        float *my = turn + (warp - 2) * P_TURN;
-        const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
-        // chunk c of this warp's NB / 2 accumulator columns: 32 of them (gated: 16 of w, 16 of w_up)
-        auto load = [&](int a, int c, uint32_t (&r)[32]) {
-            const uint32_t tb = lanes + a * NB;
-            if (GATED) {
-                uint32_t lo[16], hi[16];
-                tmem_ld16x2_sync(tb + half * (NB / 4) + c * 16, tb + NB / 2 + half * (NB / 4) + c * 16, lo, hi);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) r[j] = lo[j], r[16 + j] = hi[j];
-            } else {
-                tmem_ld32_sync(tb + half * (NB / 2) + c * 32, r);
-            }
-        };
-        auto drained = [&](int a) {  // the accumulator is free for the part after next
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                if (rank == 0)
-                    mbar_arrive(&S->acce[a]);
-                else
-                    arrive_remote(peer_addr(&S->acce[a], 0));
-            }
-        };
-        // turns the chunk and finishes it, the 16-byte pieces of row r at p ^ (r % 8) so that
-        // neither side meets a bank twice
-        auto finish = [&](const PairTile &t, int c, const uint32_t (&r)[32]) {
-            const int row0 = t.mt * 256 + (int)rank * 128 + q * 32;
-#pragma unroll
-            for (int p = 0; p < 8; ++p)
-                *reinterpret_cast<uint4 *>(my + lane * 32 + ((p ^ (lane & 7)) * 4)) =
-                    make_uint4(r[4 * p], r[4 * p + 1], r[4 * p + 2], r[4 * p + 3]);
-            __syncwarp();
-            // lane l: four columns of row r0 + it * RW; the residual of four rows at a time is in flight
-            constexpr int RW = GATED ? 8 : 4;
-            const int p = GATED ? lane & 3 : lane & 7;
-            const int r0 = GATED ? lane / 8 + (lane >> 2 & 1) * 4 : lane / 8;
-            const LinCols cols(g, t.nt * BNO + half * (BNO / 2) + c * (GATED ? 16 : 32) + p * 4);
-#pragma unroll 1
-            for (int it = 0; it < 32 / RW; it += 4) {
-                float v[4][4], u[4][4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int rr = r0 + (it + j) * RW;
-                    const float4 a = *reinterpret_cast<const float4 *>(my + rr * 32 + ((p ^ (rr & 7)) * 4));
-                    v[j][0] = a.x, v[j][1] = a.y, v[j][2] = a.z, v[j][3] = a.w;
-                    if (GATED) {
-                        const float4 b = *reinterpret_cast<const float4 *>(my + rr * 32 + (((p + 4) ^ (rr & 7)) * 4));
-                        u[j][0] = b.x, u[j][1] = b.y, u[j][2] = b.z, u[j][3] = b.w;
-                    }
-                }
-                lin_finish<GATED>(g, cols, row0 + r0 + it * RW, RW, g.M, v, u);
-            }
-            __syncwarp();
-        };
-        int n = 0;
-        bool ok = true;
-        for (int i = first; ok && i < tiles; i += step) {
-            const PairTile t = pair_tile(i, mtiles, ntiles);
-            if (!PROMOTE) {
-                const int a = n & 1;
-                if (!wait2(&S->accf[a], n / 2 & 1, g.wait_ns)) {
-                    ok = false;
-                    break;
-                }
-                ++n;
-                __syncwarp();
-                tc_fence_after();
-#pragma unroll 1
-                for (int c = 0; c < NB / 64; ++c) {
-                    uint32_t r[32];
-                    load(a, c, r);
-                    if (c == NB / 64 - 1) drained(a);
-                    finish(t, c, r);
-                }
-                continue;
-            }
-            float sum[NB / 2];
-#pragma unroll
-            for (int j = 0; j < NB / 2; ++j) sum[j] = 0.0f;
-            for (int k0 = 0; k0 < kstages; k0 += part, ++n) {
-                const int a = n & 1;
-                if (!wait2(&S->accf[a], n / 2 & 1, g.wait_ns)) {
-                    ok = false;
-                    break;
-                }
-                __syncwarp();
-                tc_fence_after();
-#pragma unroll
-                for (int c = 0; c < NB / 64; ++c) {
-                    uint32_t r[32];
-                    load(a, c, r);
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) sum[c * 32 + j] += __uint_as_float(r[j]);
-                }
-                drained(a);
-            }
-            if (!ok) break;
-#pragma unroll
-            for (int c = 0; c < NB / 64; ++c) {
-                uint32_t r[32];
-#pragma unroll
-                for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(sum[c * 32 + j]);
-                finish(t, c, r);
-            }
-        }
-        if (!ok) lin_record(g.status);
+        pair_epilogue<NB, GATED, PROMOTE>(maps, g, S, boxes + (warp - 2) * P_BOX, tmem, warp - 2, lane, rank, part);
     }
 
     tc_fence_before();
@@ -323,12 +479,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
         tc_fence_after();
         tmem_dealloc_pair(tmem, 2 * NB);
     }
-    __syncthreads();
-    if (threadIdx.x == 0) {  // leave only after the other CTA is done with this one
-        arrive_remote(peer_addr(&S->bye, rank ^ 1u));
-        if (!wait2(&S->bye, 0)) lin_record(g.status);
-    }
-    __syncthreads();
+    // leave only after the other CTA is done with this one (nothing is published: relaxed)
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 template <int NB, bool GATED, bool PROMOTE>
@@ -355,19 +507,17 @@ cudaError_t launch_pair(const LinMaps &maps, const LinArgs &g, cudaStream_t st)
     return launch_pdl(kern, dim3(2 * clusters), dim3(P_THREADS), kPairSmem<NB>, st, maps, g);
 }
 
-template <int NB>
-cudaError_t launch_pair_nb(const LinMaps &maps, const LinArgs &g, bool gated, cudaStream_t st)
-{
-    if (g.promote)
-        return gated ? launch_pair<NB, true, true>(maps, g, st) : launch_pair<NB, false, true>(maps, g, st);
-    return gated ? launch_pair<NB, true, false>(maps, g, st) : launch_pair<NB, false, false>(maps, g, st);
-}
 
 }  // namespace
 
 cudaError_t launch_linear_pair(const LinMaps &maps, const LinArgs &g, bool gated, int nb, cudaStream_t st)
 {
-    return nb == 256 ? launch_pair_nb<256>(maps, g, gated, st) : launch_pair_nb<128>(maps, g, gated, st);
+    if (g.promote) {  // the sums of a 256-column tile would not fit the epilogue's registers
+        if (nb != 128) return cudaErrorInvalidValue;
+        return gated ? launch_pair<128, true, true>(maps, g, st) : launch_pair<128, false, true>(maps, g, st);
+    }
+    if (nb == 256) return gated ? launch_pair<256, true, false>(maps, g, st) : launch_pair<256, false, false>(maps, g, st);
+    return gated ? launch_pair<128, true, false>(maps, g, st) : launch_pair<128, false, false>(maps, g, st);
 }
 
 }  // namespace moe

@@ -344,6 +344,18 @@ bool encode_sw128_bf16(CUtensorMap *m, const void *base, uint32_t rank, const ui
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_rows_32(CUtensorMap *m, const void *base, bool f32, uint64_t rows, uint64_t cols, uint64_t ld)
+{
+    EncodeTiledFn f = encode_fn();
+    if (!f) return false;
+    const cuuint64_t dims[2] = {cols, rows}, strides[1] = {ld * (f32 ? 4 : 2)};
+    const cuuint32_t box[2] = {32, 32}, es[2] = {1, 1};
+    return f(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base),
+             dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 void wait_settings(uint64_t *wait_ns, int *stall_test)
 {
     const unsigned long long wl = g_wait_ns.load();

@@ -436,6 +436,11 @@ void wait_settings(uint64_t *wait_ns, int *stall_test);
 bool encode_sw128_bf16(CUtensorMap *m, const void *base, uint32_t rank, const uint64_t *dims, const uint64_t *strides,
                        const uint32_t *box);
 
+// Tensor map of a matrix of fp32 or bf16 [rows, cols], rows `ld` elements (a multiple of 16
+// bytes) apart: 32 x 32 boxes, 16-byte chunk c of box row r at c ^ (r % 8) of 128-byte
+// rows (fp32) or at c ^ (r / 2 % 4) of 64-byte rows (bf16).
+bool encode_rows_32(CUtensorMap *m, const void *base, bool f32, uint64_t rows, uint64_t cols, uint64_t ld);
+
 // Tensor map of a row-major bf16 matrix [rows, cols], box_rows x 64 tiles with the
 // 128-byte swizzle (16-byte chunk c of tile row r stored at chunk c ^ (r % 8)).
 bool encode_sw128_2d_bf16(CUtensorMap *m, const void *base, uint64_t rows, uint64_t cols, uint32_t box_rows);
