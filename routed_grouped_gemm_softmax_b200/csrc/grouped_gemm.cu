@@ -44,6 +44,7 @@
 #include "combine.cuh"
 #include "moe_internal.h"
 #include "pdl.cuh"
+#include "row_store.cuh"
 #include "sm100_ptx.cuh"
 
 namespace moe {
@@ -79,7 +80,8 @@ struct Ctrl {
     uint32_t tmem_base;
 };
 
-constexpr size_t SMEM_BYTES = 1024 + (size_t)STAGES * (A_BYTES + B_BYTES) + sizeof(Ctrl);
+constexpr size_t CTRL_BYTES = (sizeof(Ctrl) + 127) / 128 * 128;
+constexpr size_t SMEM_BYTES = 1024 + (size_t)STAGES * (A_BYTES + B_BYTES) + CTRL_BYTES;
 
 __device__ __forceinline__ void record_status(int32_t *status, int code) { atomicCAS(status, 0, code); }
 
@@ -131,6 +133,7 @@ grouped_gemm_kernel(const __grid_constant__ AMaps tmA, const __grid_constant__ C
     uint8_t *sA = smem_raw + pad;
     uint8_t *sB = sA + STAGES * A_BYTES;
     Ctrl *S = reinterpret_cast<Ctrl *>(sB + STAGES * B_BYTES);
+    uint8_t *turns = reinterpret_cast<uint8_t *>(S) + CTRL_BYTES;  // the epilogue warps' buffers, with g.turn_rows
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     // n-tiles and K blocks of the gate/up items (modes 0, 3) and of the down / dense items
@@ -416,6 +419,7 @@ grouped_gemm_kernel(const __grid_constant__ AMaps tmA, const __grid_constant__ C
         // ------------------------------------------------------------ epilogue
         const int q = warp & 3;  // TMEM lane quarter this warp may read
         const int row = q * 32 + lane;
+        uint8_t *turn = g.turn_rows ? turns + (warp - 2) * kRowStoreBytes : nullptr;
         int rs = 0, acc = 0;
         uint32_t rphase = 0, aphase = 0;
         // y row of sorted row r: the row map's for the routed rows, r itself for the shared expert's
@@ -439,28 +443,27 @@ grouped_gemm_kernel(const __grid_constant__ AMaps tmA, const __grid_constant__ C
                 rows = tr.rows;
             }
             const bool row_ok = row < rows;
+            const int mine = min(32, rows - q * 32);  // this warp's rows (0 or less: none)
             if (!mbar_wait(&S->accf[acc], aphase, g.wait_ns)) { record_status(g.status, MOE_ERR_TIMEOUT); break; }
             tc_fence_after();
             const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * BN);
             if (!p1) {
-                __nv_bfloat16 *orow = g.out + (size_t)(row0 + row) * g.N;
 #pragma unroll 1
                 for (int c = 0; c < BNO0 / 32; ++c) {
                     uint32_t gr[32], ur[32];
                     tmem_ld32_sync(tb + c * 32, gr);
                     tmem_ld32_sync(tb + BNO0 + c * 32, ur);
                     const int col = nt * BNO0 + c * 32;
-                    if (row_ok && col < g.N) {
+                    if (mine > 0 && col < g.N) {
                         uint32_t pk[16];
+                        if (row_ok)  // what lies in other rows may be anything, and take the division's slow path
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             const float h0 = silu(__uint_as_float(gr[2 * i])) * __uint_as_float(ur[2 * i]);
                             const float h1 = silu(__uint_as_float(gr[2 * i + 1])) * __uint_as_float(ur[2 * i + 1]);
                             pk[i] = pack_bf16(h0, h1);
                         }
-                        uint4 *dst = reinterpret_cast<uint4 *>(orow + col);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) dst[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+                        store_rows_bf16(turn, pk, g.out, g.N, col, row0 + row, mine, lane);
                     }
                 }
             } else if (MODE == 2) {
@@ -486,25 +489,19 @@ grouped_gemm_kernel(const __grid_constant__ AMaps tmA, const __grid_constant__ C
                 const int N = MODE == 3 ? g.N2 : g.N;
                 __nv_bfloat16 *y = MODE == 3 ? g.out2 : g.out;
                 const int flat = row_ok ? flat_of(row0 + row) : 0;
-                __nv_bfloat16 *orow = y + (size_t)flat * N;
 #pragma unroll 1
                 for (int c = 0; c < BNO1 / 32; ++c) {
                     uint32_t r[32];
                     tmem_ld32_sync(tb + c * 32, r);
                     const int col = nt * BNO1 + c * 32;
-                    if (row_ok && col < N && g.y_f32) {
-                        float4 *dst = reinterpret_cast<float4 *>(g.y_f32 + (size_t)flat * N + col);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            dst[i] = make_float4(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]),
-                                                 __uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3]));
-                    } else if (row_ok && col < N) {
+                    if (mine <= 0) continue;
+                    if (col < N && g.y_f32) {
+                        store_rows_f32(turn, r, g.y_f32, N, col, flat, mine, lane);
+                    } else if (col < N) {
                         uint32_t pk[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) pk[i] = pack_bf16(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-                        uint4 *dst = reinterpret_cast<uint4 *>(orow + col);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) dst[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+                        store_rows_bf16(turn, pk, y, N, col, flat, mine, lane);
                     }
                 }
             }
@@ -562,7 +559,7 @@ static bool smem_attr_ready(int mode)
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
     std::lock_guard<std::mutex> lk(mu);
     if (done[mode] >> dev & 1ull) return true;
-    const int a = (int)SMEM_BYTES;
+    const int a = (int)SMEM_BYTES + 4 * kRowStoreBytes;
     if (mode == 2) return false;  // no dense mode: the router's tensor-core logits run in the fp8 kernel
     cudaError_t e = mode == 0   ? cudaFuncSetAttribute(grouped_gemm_kernel<0>, cudaFuncAttributeMaxDynamicSharedMemorySize, a)
                   : mode == 1 ? cudaFuncSetAttribute(grouped_gemm_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, a)
@@ -584,10 +581,11 @@ cudaError_t launch_grouped_gemm(const GemmArgs &g, const AMaps &tmA, const CUten
     static const LayerMaps nolm{};
     const SharedMaps &s = sm ? *sm : none;
     const LayerMaps &l = lm ? *lm : nolm;
+    const size_t smem = SMEM_BYTES + (g.turn_rows ? 4 * kRowStoreBytes : 0);
     switch (g.mode) {
-    case 0: return launch_pdl(grouped_gemm_kernel<0>, dim3(grid), dim3(THREADS), SMEM_BYTES, st, tmA, tmB0, tmB1, g, s, l);
-    case 1: return launch_pdl(grouped_gemm_kernel<1>, dim3(grid), dim3(THREADS), SMEM_BYTES, st, tmA, tmB0, tmB1, g, s, l);
-    default: return launch_pdl(grouped_gemm_kernel<3>, dim3(grid), dim3(THREADS), SMEM_BYTES, st, tmA, tmB0, tmB1, g, s, l);
+    case 0: return launch_pdl(grouped_gemm_kernel<0>, dim3(grid), dim3(THREADS), smem, st, tmA, tmB0, tmB1, g, s, l);
+    case 1: return launch_pdl(grouped_gemm_kernel<1>, dim3(grid), dim3(THREADS), smem, st, tmA, tmB0, tmB1, g, s, l);
+    default: return launch_pdl(grouped_gemm_kernel<3>, dim3(grid), dim3(THREADS), smem, st, tmA, tmB0, tmB1, g, s, l);
     }
 }
 

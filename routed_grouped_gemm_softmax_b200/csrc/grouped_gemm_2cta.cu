@@ -26,6 +26,7 @@
 #include "moe_internal.h"
 #include "pair_ptx.cuh"
 #include "pdl.cuh"
+#include "row_store.cuh"
 #include "sm100_ptx.cuh"
 
 namespace moe {
@@ -61,7 +62,7 @@ struct Ctrl2 {
     uint32_t tmem_base;
 };
 
-constexpr size_t SMEM2 = 1024 + (size_t)ST2 * (A2_BYTES + B2_BYTES) + sizeof(Ctrl2);
+constexpr size_t SMEM2 = 1024 + (size_t)ST2 * (A2_BYTES + B2_BYTES) + 4 * kRowStoreBytes + sizeof(Ctrl2);
 
 __device__ __forceinline__ void record2(int32_t *status, int code) { atomicCAS(status, 0, code); }
 __device__ __forceinline__ float silu2(float a) { return a / (1.0f + __expf(-a)); }
@@ -102,7 +103,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS2, 1)
     const uint32_t pad = (1024u - (smem_u32(smem2) & 1023u)) & 1023u;
     uint8_t *sA = smem2 + pad;
     uint8_t *sB = sA + ST2 * A2_BYTES;
-    Ctrl2 *S = reinterpret_cast<Ctrl2 *>(sB + ST2 * B2_BYTES);
+    uint8_t *turns = sB + ST2 * B2_BYTES;  // the epilogue warps' buffers
+    Ctrl2 *S = reinterpret_cast<Ctrl2 *>(turns + 4 * kRowStoreBytes);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = cluster_rank();
     const int NP1 = MODE == 3 ? g.N2 : g.N, KP1 = MODE == 3 ? g.K2 : g.K;  // N and K of the down items
@@ -352,6 +354,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS2, 1)
         // ------------------------------------------------ epilogue (both CTAs)
         const int q = warp & 3;
         const int row = q * 32 + lane;
+        uint8_t *turn = g.turn_rows ? turns + (warp - 2) * kRowStoreBytes : nullptr;
         int rs = 0, acc = 0;
         uint32_t rphase = 0, aphase = 0;
         // y row of sorted row r: the row map's for the routed rows, r itself for the shared expert's
@@ -372,55 +375,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS2, 1)
             const int row0 = tr.row0 + (int)rank * HALF;
             const int rows = min(HALF, max(0, tr.rows - (int)rank * HALF));
             const bool row_ok = row < rows;
+            const int mine = min(32, rows - q * 32);  // this warp's rows (0 or less: none)
             if (!wait2(&S->accf[acc], aphase, g.wait_ns)) { record2(g.status, MOE_ERR_TIMEOUT); break; }
             tc_fence_after();
             const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * BN2);
             if (!p1) {
-                __nv_bfloat16 *orow = g.out + (size_t)(row0 + row) * g.N;
 #pragma unroll 1
                 for (int c = 0; c < BNO0 / 32; ++c) {
                     uint32_t gr[32], ur[32];
                     tmem_ld32_sync(tb + c * 32, gr);
                     tmem_ld32_sync(tb + BNO0 + c * 32, ur);
                     const int col = nt * BNO0 + c * 32;
-                    if (row_ok && col < g.N) {
+                    if (mine > 0 && col < g.N) {
                         uint32_t pk[16];
+                        if (row_ok)  // what lies in other rows may be anything, and take the division's slow path
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             const float h0 = silu2(__uint_as_float(gr[2 * i])) * __uint_as_float(ur[2 * i]);
                             const float h1 = silu2(__uint_as_float(gr[2 * i + 1])) * __uint_as_float(ur[2 * i + 1]);
                             pk[i] = pack_bf16_2(h0, h1);
                         }
-                        uint4 *dst = reinterpret_cast<uint4 *>(orow + col);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            dst[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+                        store_rows_bf16(turn, pk, g.out, g.N, col, row0 + row, mine, lane);
                     }
                 }
             } else {
                 __nv_bfloat16 *y = MODE == 3 ? g.out2 : g.out;
                 const int flat = row_ok ? flat_of(row0 + row) : 0;
-                __nv_bfloat16 *orow = y + (size_t)flat * NP1;
 #pragma unroll 1
                 for (int c = 0; c < BNO1 / 32; ++c) {
                     uint32_t r[32];
                     tmem_ld32_sync(tb + c * 32, r);
                     const int col = nt * BNO1 + c * 32;
-                    if (row_ok && col < NP1 && g.y_f32) {
-                        float4 *dst = reinterpret_cast<float4 *>(g.y_f32 + (size_t)flat * NP1 + col);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            dst[i] = make_float4(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]),
-                                                 __uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3]));
-                    } else if (row_ok && col < NP1) {
+                    if (mine <= 0) continue;
+                    if (col < NP1 && g.y_f32) {
+                        store_rows_f32(turn, r, g.y_f32, NP1, col, flat, mine, lane);
+                    } else if (col < NP1) {
                         uint32_t pk[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
                             pk[i] = pack_bf16_2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-                        uint4 *dst = reinterpret_cast<uint4 *>(orow + col);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            dst[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+                        store_rows_bf16(turn, pk, y, NP1, col, flat, mine, lane);
                     }
                 }
             }

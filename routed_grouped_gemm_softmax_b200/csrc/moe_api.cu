@@ -529,6 +529,7 @@ moe_status_t forward_bf16(const moe_dims_t *d, const void *x, const void *router
     const unsigned long long wl = g_wait_ns.load();
     const uint64_t wait_ns = wl ? wl : 2000000000ull;
     const int stall = g_stall_test.load();
+    const bool turn_rows = A / d->E >= 32;  // tiles with full warps of rows, on average
     // the gate/up and the down GEMM in one persistent launch (readiness counters per
     // m-tile hand h from one to the other)
     const bool layer = plan & MOE_PLAN_LAYER_GEMM;
@@ -545,6 +546,7 @@ moe_status_t forward_bf16(const moe_dims_t *d, const void *x, const void *router
         gl.N2 = d->H;
         gl.out2 = y;
         gl.ready = at<int32_t>(ws, L.ready);
+        gl.turn_rows = turn_rows;
         gl.y_f32 = given ? at<float>(ws, L.y) : nullptr;
         if (direct) {
             gl.a_rows = s2f;
@@ -565,6 +567,7 @@ moe_status_t forward_bf16(const moe_dims_t *d, const void *x, const void *router
     if (e == cudaSuccess && !layer) {
         moe::GemmArgs g1{0, d->H, d->I, tiles, ntiles, &hdr->counter[0], &hdr->status, h, nullptr, ctas, rev, wait_ns, stall};
         g1.trace = trace1;
+        g1.turn_rows = turn_rows;
         g1.sh_count = sh;
         g1.sh_T = d->T;
         g1.sh_rows0 = A;
@@ -585,6 +588,7 @@ moe_status_t forward_bf16(const moe_dims_t *d, const void *x, const void *router
                          stall, 0, nullptr, gate, fused ? at<int32_t>(ws, L.ccnt) : nullptr,
                          static_cast<__nv_bfloat16 *>(out), d->top_k, d->top_k + sh};
         g2.trace = trace2;
+        g2.turn_rows = turn_rows;
         g2.y_f32 = given ? at<float>(ws, L.y) : nullptr;
         g2.sh_count = sh;
         g2.sh_T = d->T;

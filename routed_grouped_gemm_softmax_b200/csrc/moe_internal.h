@@ -226,6 +226,8 @@ struct GemmArgs {
     // Down items with y_f32 non-null: y rows are written there in fp32 instead of in bf16 to
     // out (mode 1) or out2 (mode 3); no fused combine.
     float *y_f32;
+    // Full warps of h and y rows are turned in shared memory before they are stored (row_store.cuh).
+    bool turn_rows;
 };
 
 // Tensor maps of the down half of the fused layer GEMM (mode 3): h as its A operand
