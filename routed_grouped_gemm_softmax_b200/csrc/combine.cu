@@ -38,24 +38,34 @@ __device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&v)[8])
 }
 
 // out[t] = bf16(sum of w[t,j] y[t*k + j] over the slots j with an expert), fp32 fma in
-// ascending j.  A slot without an expert has no y row: its memory is not read.
+// ascending j.  A slot without an expert has no y row: its memory is not read.  Bound by the
+// rows' latency where they are loaded one by one (2048 tokens, k 6, H 2048: 18.4 us, 88 MB).
 template <typename TY>
-__global__ void __launch_bounds__(256) combine_given_kernel(const TY *__restrict__ y, const int32_t *__restrict__ idx,
-                                                            const float *__restrict__ w, int H, int E, int k,
-                                                            __nv_bfloat16 *__restrict__ out)
+__global__ void __launch_bounds__(256) combine_given_kernel(const TY *y, const int32_t *idx, const float *w, int H, int E,
+                                                            int k, __nv_bfloat16 *out)
 {
+    constexpr int U = 4;
     pdl_wait();
     pdl_trigger();
     const size_t t = blockIdx.x;
     for (int c = threadIdx.x * 8; c < H; c += 256 * 8) {
         float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        for (int j = 0; j < k; ++j) {
-            if ((unsigned)idx[t * k + j] >= (unsigned)E) continue;
-            const float g = w[t * k + j];
-            float v[8];
-            load8(y + (t * k + j) * H + c, v);
+        for (int j0 = 0; j0 < k; j0 += U) {  // U rows are under way at once
+            float v[U][8], g[U];
+            bool any[U];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) acc[i] = fmaf(g, v[i], acc[i]);
+            for (int j = 0; j < U; ++j) {
+                any[j] = j0 + j < k && (unsigned)idx[t * k + min(j0 + j, k - 1)] < (unsigned)E;
+                g[j] = any[j] ? w[t * k + j0 + j] : 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+                if (any[j]) load8(y + (t * k + j0 + j) * H + c, v[j]);
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+                if (any[j])
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) acc[i] = fmaf(g[j], v[j][i], acc[i]);
         }
         uint4 o;
         __nv_bfloat162 *q = reinterpret_cast<__nv_bfloat162 *>(&o);

@@ -439,6 +439,14 @@ cudaError_t group_assignments(const moe_dims_t &d, const moe::WsLayout &L, const
                               const StageMarks &marks, cudaStream_t st)
 {
     cudaError_t e = cudaSuccess;
+    if (given && moe::permute_one_ok(d)) {  // no fused combine: its counts are not read
+        e = marks.mark(1, st);
+        if (e != cudaSuccess) return e;
+        return moe::launch_permute_one(d, given->idx, at<int32_t>(ws, L.offsets), at<int32_t>(ws, L.s2f),
+                                       at<int32_t>(ws, L.f2s), at<int32_t>(ws, L.tiles), at<int32_t>(ws, L.ntiles),
+                                       at<int32_t>(ws, L.tiles2), at<int32_t>(ws, L.ntiles2), hdr,
+                                       at<int32_t>(ws, L.ready), (int)((L.clear_bytes - L.ready) / 4), st, true);
+    }
     if (given || !moe::small_route_permute_ok(d))  // else the router's kernels clear them
         e = cudaMemsetAsync(hdr, 0, L.clear_bytes, st);
     if (e != cudaSuccess) return e;
@@ -513,8 +521,9 @@ moe_status_t forward_bf16(const moe_dims_t *d, const void *x, const void *router
     const bool direct = plan & MOE_PLAN_DIRECT_A;
     if (direct && !encode_2d(&sm1.xg, x, d->T, d->H, 1)) return MOE_ERR_CUDA;
     // the tile list is then the output of the kernel just before the gate/up GEMM
-    // when the router and the grouping are one launch
-    const int tiles_first = direct && (plan & MOE_PLAN_SMALL_ROUTER) ? 1 : 0;
+    // when the router and the grouping, or the whole grouping, are one launch
+    const bool one = given ? moe::permute_one_ok(*d) : (plan & MOE_PLAN_SMALL_ROUTER) != 0;
+    const int tiles_first = direct && one ? 1 : 0;
 
     const StageMarks marks;
     const bool fused = plan & MOE_PLAN_FUSED_COMBINE;  // combine inside the down GEMM

@@ -150,6 +150,15 @@ cudaError_t launch_permute(const moe_dims_t &d, const WsLayout &L, const int32_t
                            cudaStream_t st, int32_t *tiles2 = nullptr, int32_t *ntiles2 = nullptr,
                            bool none_ok = false);
 
+// The same by one block, which clears the header and the `nready` counts at `ready` first: for lists
+// of up to kPermOneMaxA entries (4 steps a warp: 12288 took 21 us against 16 of a memset and the
+// three kernels, 128 5.8 against 11) whose counts of 32 warps fit the default shared memory.
+constexpr int kPermOneMaxA = 4096;
+bool permute_one_ok(const moe_dims_t &d);
+cudaError_t launch_permute_one(const moe_dims_t &d, const int32_t *idx, int32_t *offsets, int32_t *s2f, int32_t *f2s,
+                               int32_t *tiles, int32_t *ntiles, int32_t *tiles2, int32_t *ntiles2, WsHeader *hdr,
+                               int32_t *ready, int nready, cudaStream_t st, bool none_ok);
+
 // xs[f2s[f]] = x[f / k] for every assignment f = t*k + j (a warp per assignment, flat order).
 cudaError_t launch_gather_rows(const __nv_bfloat16 *x, const int32_t *f2s, int T, int H, int top_k,
                                __nv_bfloat16 *xs, cudaStream_t st);

@@ -160,6 +160,93 @@ __global__ void perm_scatter_kernel(const int32_t *__restrict__ idx, int A, int 
     f2s[f] = pos;
 }
 
+// The three passes, and the clearing that comes before them, by one block: warp w has the w-th of
+// 32 runs of the list, hist[w][e] its count of expert e and then the row of its next entry.
+__global__ void __launch_bounds__(1024)
+perm_one_kernel(const int32_t *idx, int A, int E, int32_t *offsets, int32_t *s2f, int32_t *f2s, int32_t *tiles,
+                int32_t *ntiles, int32_t *tiles2, int32_t *ntiles2, WsHeader *hdr, int32_t *ready, int nready,
+                int none_ok)
+{
+    pdl_wait();
+    pdl_trigger();
+    extern __shared__ int hist[];
+    __shared__ int warp_tot[33];
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    for (int i = tid; i < 32 * E; i += 1024) hist[i] = 0;
+    for (int i = tid; i < nready; i += 1024) ready[i] = 0;
+    if (tid < 8) tid ? hdr->counter[tid - 1] = 0 : hdr->status = 0;
+    __syncthreads();
+    const int run = (A + 1023) / 1024 * 32, f0 = warp * run, f1 = min(A, f0 + run);
+    int *mine = hist + warp * E;
+#pragma unroll 4
+    for (int f = f0 + lane; f < f1; f += 32) {
+        const int e = idx[f];
+        if (e >= 0 && e < E)
+            atomicAdd(mine + e, 1);
+        else if (!(none_ok && e == -1))
+            record_status(&hdr->status, MOE_ERR_BAD_INDEX);
+    }
+    __syncthreads();
+    int cnt = 0;
+    if (tid < E)
+#pragma unroll 8
+        for (int w = 0; w < 32; ++w) {
+            const int c = hist[w * E + tid];
+            hist[w * E + tid] = cnt;
+            cnt += c;
+        }
+    int total_rows = 0, total_tiles = 0, total_pairs = 0;
+    const int off = block_exclusive_scan(cnt, warp_tot, total_rows);
+    const int nt = (cnt + kTileRows - 1) / kTileRows, np = (cnt + 2 * kTileRows - 1) / (2 * kTileRows);
+    const int tstart = block_exclusive_scan(nt, warp_tot, total_tiles);
+    const int pstart = block_exclusive_scan(np, warp_tot, total_pairs);
+    if (tid < E) {
+        offsets[tid] = off;
+#pragma unroll 8
+        for (int w = 0; w < 32; ++w) hist[w * E + tid] += off;
+        for (int m = 0; m < nt; ++m) {
+            int32_t *tl = tiles + 3 * (size_t)(tstart + m);
+            tl[0] = tid;
+            tl[1] = off + m * kTileRows;
+            tl[2] = min(kTileRows, cnt - m * kTileRows);
+        }
+        for (int m = 0; m < np; ++m) {
+            int32_t *tl = tiles2 + 3 * (size_t)(pstart + m);
+            tl[0] = tid;
+            tl[1] = off + m * 2 * kTileRows;
+            tl[2] = min(2 * kTileRows, cnt - m * 2 * kTileRows);
+        }
+    }
+    if (tid == 0) {
+        offsets[E] = total_rows;
+        *ntiles = total_tiles;
+        *ntiles2 = total_pairs;
+    }
+    __syncthreads();
+    int e = f0 + lane < f1 ? idx[f0 + lane] : -1;
+#pragma unroll 1
+    for (int f = f0 + lane; f - lane < f1; f += 32) {
+        const int next = f + 32 < f1 ? idx[f + 32] : -1;
+        const bool valid = e >= 0 && e < E;
+        const unsigned peers = __match_any_sync(0xffffffffu, valid ? e : -1);
+        const int rank = __popc(peers & ((1u << lane) - 1u));
+        if (valid) {
+            const int pos = mine[e] + rank;
+            s2f[pos] = f;
+            f2s[f] = pos;
+        } else if (none_ok && f < f1) {
+            f2s[f] = -1;
+        }
+        __syncwarp();
+        if (valid && rank == 0) mine[e] += __popc(peers);
+        __syncwarp();
+        e = next;
+    }
+    // skipped entries leave the tail of s2f without a row: flat row 0, which exists
+    if (none_ok)
+        for (int f = total_rows + tid; f < A; f += 1024) s2f[f] = 0;
+}
+
 // x rows into expert-sorted order, a warp per assignment in flat order: warp f
 // copies x[f / k] to xs[f2s[f]].  The k copies of a token are made by neighbouring
 // warps, close in time, so x is read from DRAM about once; walking the sorted rows
@@ -198,6 +285,19 @@ cudaError_t launch_permute(const moe_dims_t &d, const WsLayout &L, const int32_t
         e = launch_pdl(perm_scatter_kernel, dim3(L.nb), dim3(L.chunk), (size_t)(L.chunk / 32) * E * sizeof(int), st,
                        idx, A, E, blk_base, s2f, f2s, (int)none_ok, offsets);
     return e;
+}
+
+bool permute_one_ok(const moe_dims_t &d)
+{
+    return (long long)d.T * d.top_k <= kPermOneMaxA && 32 * d.E * sizeof(int) <= 47 * 1024;
+}
+
+cudaError_t launch_permute_one(const moe_dims_t &d, const int32_t *idx, int32_t *offsets, int32_t *s2f, int32_t *f2s,
+                               int32_t *tiles, int32_t *ntiles, int32_t *tiles2, int32_t *ntiles2, WsHeader *hdr,
+                               int32_t *ready, int nready, cudaStream_t st, bool none_ok)
+{
+    return launch_pdl(perm_one_kernel, dim3(1), dim3(1024), 32 * d.E * sizeof(int), st, idx, d.T * d.top_k, d.E,
+                      offsets, s2f, f2s, tiles, ntiles, tiles2, ntiles2, hdr, ready, nready, (int)none_ok);
 }
 
 cudaError_t launch_gather_rows(const __nv_bfloat16 *x, const int32_t *f2s, int T, int H, int top_k,
