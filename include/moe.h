@@ -224,8 +224,8 @@ moe_status_t moe_forward_shared(const moe_dims_t *d, const void *x, const void *
  * Rows are ldx, ldw (w and w_up), ldr, ldo elements apart.  gelu is the erf form v Phi(v),
  * gelu_tanh its tanh approximation, silu v / (1 + exp(-v)).  Products are summed in
  * fp32 on the tensor cores and everything after them in fp32; out is rounded once.  The order
- * of every sum is fixed by the dims.  out may be residual itself (same rows); it may
- * overlap nothing else that the call reads.
+ * of every sum is fixed by the sizes, the types and the device.  out may be residual itself
+ * (same rows); it may overlap nothing else that the call reads.
  * The workspace holds moe_linear_workspace_size() bytes, 256-byte aligned, that are
  * ZERO before its first call; calls leave it zero unless a pipeline wait ran out, which
  * moe_get_device_status(ws, stream) reports and clears.

@@ -198,7 +198,7 @@ def _call(fn, where, dev, stream, *args):
         raise ValueError(f"{where}: a stream of {stream.device} for tensors on {dev}")
     else:
         handle = stream.cuda_stream
-    if torch.cuda.current_device() == dev.index:
+    if torch._C._cuda_getDevice() == dev.index:
         code = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
@@ -468,8 +468,9 @@ def moe_linear(x, w, bias=None, act: str = "none", residual=None, w_up=None, bia
         raise ValueError(f"act {act!r} (of {list(ACTS)}), out_dtype {out_dtype} (bf16 or fp32)")
     ldr = 0 if residual is None else _rows_of(residual, dev, (out_dtype,), (M, N), "residual")
     if out is None:
-        out = _empty((M, N), out_dtype, x, stream)
-    ldo = _rows_of(out, dev, (out_dtype,), (M, N), "out")
+        out, ldo = _empty((M, N), out_dtype, x, stream), N
+    else:
+        ldo = _rows_of(out, dev, (out_dtype,), (M, N), "out")
     if ws is None:
         ws = linear_workspace(dev, stream)
     elif ws.device != dev:
