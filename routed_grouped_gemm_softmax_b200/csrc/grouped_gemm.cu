@@ -16,15 +16,15 @@
 // section 03).
 //
 // CTA roles (192 threads):
-//   warp 0, lane 0: claims items, feeds a ring of item ids to the other roles,
-//                   and streams A and B tiles into a 4-stage shared-memory ring
-//                   with TMA (128-byte swizzle), one mbarrier pair per stage;
+//   warp 0        : lane 0 claims items and feeds a ring of item ids to the other roles;
+//                   the warp streams A tiles and B half tiles into shared-memory rings
+//                   with TMA (128-byte swizzle), one mbarrier pair per slot;
 //                   with direct A rows, the 32 lanes each gather four x rows of
 //                   a gate/up tile per stage (tile::gather4), so no expert-ordered
 //                   copy of x is written;
-//   warp 1        : allocates 512 TMEM columns; lane 0 issues tcgen05.mma
-//                   (M=128, N=256, K=16, bf16 in, fp32 accumulate) into one of
-//                   two TMEM accumulators, releasing each stage with
+//   warp 1        : allocates 512 TMEM columns; an elected lane issues tcgen05.mma
+//                   (M=128, N=128, K=16, bf16 in, fp32 accumulate) into the halves of one
+//                   of two TMEM accumulators, releasing each slot with
 //                   tcgen05.commit;
 //   warps 2-5     : epilogue -- tcgen05.ld of the accumulator (each warp reads
 //                   its 32-lane quarter), then
@@ -45,7 +45,7 @@
 #include "moe_internal.h"
 #include "pdl.cuh"
 #include "row_store.cuh"
-#include "sm100_ptx.cuh"
+#include "warp_ptx.cuh"
 
 namespace moe {
 namespace {
@@ -55,21 +55,29 @@ constexpr int BK = 64;         // a K chunk: 64 bf16 = one 128-byte swizzle row
 constexpr int KC = 2;          // K chunks per stage
 constexpr int BKS = BK * KC;   // K of a stage: 128
 constexpr int BN = 256;        // output columns per item (gate/up: 128 + 128)
-// Two stages of 128 K columns (96 KB) rather than four of 64: each weight box then
-// brings both chunks of its rows, 256 contiguous bytes a row, which DRAM streams about
-// a third faster than 128-byte row pieces, and fewer bytes wait on more barriers.
-constexpr int STAGES = 2;
+// Stages of 128 K columns: each weight box then brings both chunks of its rows, 256
+// contiguous bytes a row, which DRAM streams about a third faster than 128-byte row
+// pieces.  A stage's A rows and the two halves of its B rows (gate and up, or 128 + 128
+// output columns) have rings and barriers of their own: a half is refilled while the other
+// is multiplied (1024 tokens, k 4 of 64 experts: the call 98.8 us with one barrier for
+// the 96 KB of a stage, 93.6 so; 16 tokens, k 8 of 256: 77.0 and 75.0).  The finer steps need
+// converged producer and MMA warps: by lane 0 alone they were slower, 99.9 us.
+constexpr int STAGES = 2;       // A slots
+constexpr int BSLOTS = 4;       // B half slots
 constexpr int RING = 4;
 constexpr int A_SUB = BM * BK * 2;     // 16 KB: one chunk of A rows
 constexpr int B_SUB = BN * BK * 2;     // 32 KB: one chunk of B rows
 constexpr int A_BYTES = A_SUB * KC;    // 32 KB
-constexpr int B_BYTES = B_SUB * KC;    // 64 KB
+constexpr int H_SUB = B_SUB / 2;       // 16 KB: one chunk of half the B rows
+constexpr int H_BYTES = H_SUB * KC;    // 32 KB
 constexpr int THREADS = 192;
 constexpr uint32_t TMEM_COLS = 512;   // two 128 x 256 fp32 accumulators
 
 struct Ctrl {
-    uint64_t full[STAGES];   // TMA bytes landed in stage s
-    uint64_t empty[STAGES];  // MMAs reading stage s finished
+    uint64_t full[STAGES];   // TMA bytes landed in A slot s
+    uint64_t empty[STAGES];  // MMAs reading A slot s finished
+    uint64_t bfull[BSLOTS];  // the same of B slot s
+    uint64_t bempty[BSLOTS];
     uint64_t accf[2];        // accumulator a holds a finished tile
     uint64_t acce[2];        // epilogue drained accumulator a
     uint64_t itf[RING];      // ring slot r holds the next item id
@@ -81,7 +89,7 @@ struct Ctrl {
 };
 
 constexpr size_t CTRL_BYTES = (sizeof(Ctrl) + 127) / 128 * 128;
-constexpr size_t SMEM_BYTES = 1024 + (size_t)STAGES * (A_BYTES + B_BYTES) + CTRL_BYTES;
+constexpr size_t SMEM_BYTES = 1024 + (size_t)STAGES * A_BYTES + (size_t)BSLOTS * H_BYTES + CTRL_BYTES;
 
 __device__ __forceinline__ void record_status(int32_t *status, int code) { atomicCAS(status, 0, code); }
 
@@ -132,10 +140,10 @@ grouped_gemm_kernel(const __grid_constant__ AMaps tmA, const __grid_constant__ C
     const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
     uint8_t *sA = smem_raw + pad;
     uint8_t *sB = sA + STAGES * A_BYTES;
-    Ctrl *S = reinterpret_cast<Ctrl *>(sB + STAGES * B_BYTES);
+    Ctrl *S = reinterpret_cast<Ctrl *>(sB + BSLOTS * H_BYTES);
     uint8_t *turns = reinterpret_cast<uint8_t *>(S) + CTRL_BYTES;  // the epilogue warps' buffers, with g.turn_rows
 
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = uniform_warp(), lane = threadIdx.x % 32;
     // n-tiles and K blocks of the gate/up items (modes 0, 3) and of the down / dense items
     const int nt0 = (g.N + BNO0 - 1) / BNO0, kb0 = (g.K + BKS - 1) / BKS;
     const int nt1 = MODE == 3 ? (g.N2 + BNO1 - 1) / BNO1 : (g.N + BNO1 - 1) / BNO1;
@@ -148,6 +156,10 @@ grouped_gemm_kernel(const __grid_constant__ AMaps tmA, const __grid_constant__ C
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&S->full[s], 1);
             mbar_init(&S->empty[s], 1);
+        }
+        for (int s = 0; s < BSLOTS; ++s) {
+            mbar_init(&S->bfull[s], 1);
+            mbar_init(&S->bempty[s], 1);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&S->accf[a], 1);
@@ -174,7 +186,7 @@ grouped_gemm_kernel(const __grid_constant__ AMaps tmA, const __grid_constant__ C
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = S->tmem_base;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, S->tmem_base, 0);
     // The prologue above overlapped the previous kernel.  Modes 0, 1 and 3: warp 0
     // waits for it inside the producer, after the first stages' weight loads (the
     // weights are the layer's inputs; only the A rows are the previous kernel's output).
@@ -208,9 +220,13 @@ grouped_gemm_kernel(const __grid_constant__ AMaps tmA, const __grid_constant__ C
         // routed gate/up tile per stage, lane l rows 4l..4l+3.
         const bool gather = (MODE == 0 || MODE == 3) && g.a_rows != nullptr;
         const int total = MODE == 3 ? total0 + mtiles * nt1 : mtiles * (MODE == 0 ? nt0 : nt1);
-        int stage = 0, rs = 0;
-        uint32_t phase = 0, rphase = 0;
-        uint32_t armed = 0, armed_par = 0;  // stages with a load issued, and its phase
+        int stage = 0, bs = 0, rs = 0;
+        uint32_t phase = 0, bphase = 0, rphase = 0;
+        uint32_t armed = 0, armed_par = 0;  // slots (A, then B) with a load issued, and its phase
+        auto arm = [&](uint32_t bit, uint32_t ph) {
+            armed |= 1u << bit;
+            armed_par = (armed_par & ~(1u << bit)) | (ph << bit);
+        };
         bool ok = true;
         int cursor = (int)blockIdx.x * (g.reverse == 2);  // static modes
         bool held = early_b;  // A loads of the first item's first stages wait for the previous kernel
@@ -291,36 +307,38 @@ grouped_gemm_kernel(const __grid_constant__ AMaps tmA, const __grid_constant__ C
             }
             for (int kb = 0; kb < num_kb; ++kb) {
                 const int nc = chunks_of(kb, Kd);
-                if (lane == 0) {
-                    okl = mbar_wait(&S->empty[stage], phase ^ 1, g.wait_ns);
-                    if (okl) {
-                        mbar_arrive_expect_tx(&S->full[stage], a_bytes * nc + B_BYTES);
-                        armed |= 1u << stage;
-                        armed_par = (armed_par & ~(1u << stage)) | (phase << stage);
-                        uint8_t *b_dst = sB + stage * B_BYTES;
-                        const int z = kb * KC;  // first K chunk of the stage
-                        if (!held && !g4)
-                            for (int c = 0; c < nc; ++c)
-                                tma_load_2d(sA + stage * A_BYTES + c * A_SUB, amap, &S->full[stage], (z + c) * BK, arow0);
-                        if (!p1) {  // gate / up rows n0.. of the expert (or of shared slice s): [KC][128] each
-                            if (tr.s < 0) {
-                                tma_load_4d(b_dst, &tmB0, &S->full[stage], 0, n0, z, expert);
-                                tma_load_4d(b_dst + B_BYTES / 2, &tmB1, &S->full[stage], 0, n0, z, expert);
-                            } else {
-                                tma_load_3d(b_dst, &sm.b0, &S->full[stage], 0, tr.s * g.N + n0, z);
-                                tma_load_3d(b_dst + B_BYTES / 2, &sm.b1, &S->full[stage], 0, tr.s * g.N + n0, z);
-                            }
-                        } else {  // down rows n0..: the expert's, or chunks of columns s*I.. of the shared down: [KC][256]
-                            const CUtensorMap *bm = MODE == 3 ? &lm.wd : &tmB0;
-                            const CUtensorMap *bs = MODE == 3 ? &lm.wd_sh : &sm.b0;
-                            if (tr.s < 0)
-                                tma_load_4d(b_dst, bm, &S->full[stage], 0, n0, z, expert);
-                            else
-                                tma_load_3d(b_dst, bs, &S->full[stage], 0, n0, tr.s * (K1 / BK) + z);
-                        }
-                    }
+                if (!warp_wait(&S->empty[stage], phase ^ 1, g.wait_ns)) { ok = false; break; }
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&S->full[stage], a_bytes * nc);
+                    if (!held && !g4)
+                        for (int c = 0; c < nc; ++c)
+                            tma_load_2d(sA + stage * A_BYTES + c * A_SUB, amap, &S->full[stage], (kb * KC + c) * BK, arow0);
                 }
-                if (!__shfl_sync(0xffffffffu, okl, 0)) { ok = false; break; }
+                __syncwarp();
+                arm(stage, phase);
+                const int z = kb * KC;  // first K chunk of the stage
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    if (!warp_wait(&S->bempty[bs], bphase ^ 1, g.wait_ns)) { ok = false; break; }
+                    uint64_t *bar = &S->bfull[bs];
+                    uint8_t *dst = sB + bs * H_BYTES;
+                    // gate / up rows n0.. of the expert (or of shared slice s), [KC][128], or down rows
+                    // n0 + 128 half..: the expert's, or chunks of columns s*I.. of the shared down
+                    const CUtensorMap *bm = !p1 ? half ? &tmB1 : &tmB0 : MODE == 3 ? &lm.wd : &tmB0;
+                    const CUtensorMap *bsh = !p1 ? half ? &sm.b1 : &sm.b0 : MODE == 3 ? &lm.wd_sh : &sm.b0;
+                    const int brow = p1 ? n0 + half * (BN / 2) : n0;
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(bar, H_BYTES);
+                        if (tr.s < 0)
+                            tma_load_4d(dst, bm, bar, 0, brow, z, expert);
+                        else
+                            tma_load_3d(dst, bsh, bar, 0, p1 ? brow : tr.s * g.N + brow, p1 ? tr.s * (K1 / BK) + z : z);
+                    }
+                    __syncwarp();
+                    arm(STAGES + bs, bphase);
+                    if (++bs == BSLOTS) { bs = 0; bphase ^= 1; }
+                }
+                if (!ok) break;
                 if (g4_lane && !held)
                     for (int c = 0; c < nc; ++c)
                         tma_gather4(sA + stage * A_BYTES + c * A_SUB + lane * 512, &sm.xg, &S->full[stage],
@@ -351,69 +369,71 @@ grouped_gemm_kernel(const __grid_constant__ AMaps tmA, const __grid_constant__ C
                 }
             }
             // never leave with TMA copies still landing in shared memory
-            for (int s = 0; s < STAGES; ++s)
+            for (int s = 0; s < STAGES + BSLOTS; ++s)
                 if ((armed >> s) & 1u)
-                    if (!mbar_wait(&S->full[s], (armed_par >> s) & 1u)) record_status(g.status, MOE_ERR_TIMEOUT);
+                    if (!mbar_wait(s < STAGES ? &S->full[s] : &S->bfull[s - STAGES], (armed_par >> s) & 1u))
+                        record_status(g.status, MOE_ERR_TIMEOUT);
         }
         __syncwarp();
     } else if (warp == 1) {
         // ---------------------------------------------------------- MMA issuer
-        if (lane == 0) {
-            constexpr uint32_t IDESC = idesc_bf16_f32(BM, BN);           // down: N = 256
-            constexpr uint32_t IDESC_H = idesc_bf16_f32(BM, BN / 2);     // gate, up: N = 128 each
-            int stage = 0, rs = 0, acc = 0;
-            uint32_t phase = 0, rphase = 0, aphase = 0;
-            // timeout test: wait (bounded) on a barrier nothing signals, then unwind
-            bool ok = !(g.stall_test && !mbar_wait(&S->never, 0, g.wait_ns));
-            while (ok) {
-                if (!mbar_wait(&S->itf[rs], rphase, g.wait_ns)) { ok = false; break; }
-                const int item = S->ring[rs];
-                mbar_arrive(&S->ite[rs]);
-                if (++rs == RING) { rs = 0; rphase ^= 1; }
-                if (item < 0) break;
-                const bool p1 = pos_of(item).p1;
-                const int num_kb = p1 ? kb1 : kb0, Kd = p1 ? K1 : g.K;
-                if (!mbar_wait(&S->acce[acc], aphase ^ 1, g.wait_ns)) { ok = false; break; }
-                tc_fence_after();
-                const uint32_t d = tmem + static_cast<uint32_t>(acc * BN);
-                for (int kb = 0; kb < num_kb; ++kb) {
-                    if (!mbar_wait(&S->full[stage], phase, g.wait_ns)) { ok = false; break; }
+        // (the whole warp, converged: warp_ptx.cuh)
+        constexpr uint32_t IDESC = idesc_bf16_f32(BM, BN / 2);  // gate, up, or 128 down columns
+        const uint32_t sA0 = smem_u32(sA), sB0 = smem_u32(sB);
+        int stage = 0, bs = 0, rs = 0, acc = 0;
+        uint32_t phase = 0, bphase = 0, rphase = 0, aphase = 0;
+        // timeout test: wait (bounded) on a barrier nothing signals, then unwind
+        bool ok = !(g.stall_test && !warp_wait(&S->never, 0, g.wait_ns));
+        while (ok) {
+            if (!warp_wait(&S->itf[rs], rphase, g.wait_ns)) { ok = false; break; }
+            const int item = __shfl_sync(0xffffffffu, S->ring[rs], 0);
+            if (elect_one()) mbar_arrive(&S->ite[rs]);
+            __syncwarp();
+            if (++rs == RING) { rs = 0; rphase ^= 1; }
+            if (item < 0) break;
+            const bool p1 = pos_of(item).p1;
+            const int num_kb = p1 ? kb1 : kb0, Kd = p1 ? K1 : g.K;
+            if (!warp_wait(&S->acce[acc], aphase ^ 1, g.wait_ns)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t d = tmem + static_cast<uint32_t>(acc * BN);
+            for (int kb = 0; ok && kb < num_kb; ++kb) {
+                const uint32_t a0 = sA0 + stage * A_BYTES;
+                const int nc = chunks_of(kb, Kd);
+                if (!warp_wait(&S->full[stage], phase, g.wait_ns)) { ok = false; break; }
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    // gate (or the first 128) columns 0..127 of the accumulator, up (or the next 128) 128..255
+                    if (!warp_wait(&S->bfull[bs], bphase, g.wait_ns)) { ok = false; break; }
                     tc_fence_after();
-                    const uint32_t a0 = smem_u32(sA + stage * A_BYTES);
-                    const uint32_t b0 = smem_u32(sB + stage * B_BYTES);
-                    const int nc = chunks_of(kb, Kd);
-                    for (int c = 0; c < nc; ++c) {
-                        const uint32_t ac = a0 + c * A_SUB;
-                        if (!p1) {
-                            // gate rows [KC][128] then up rows [KC][128]: an N = 128 MMA into
-                            // each half of the accumulator (gate columns 0..127, up 128..255)
-                            const uint32_t bg = b0 + c * (B_SUB / 2), bu = b0 + B_BYTES / 2 + c * (B_SUB / 2);
+                    const uint32_t b0 = sB0 + bs * H_BYTES;
+                    if (elect_one()) {
 #pragma unroll
-                            for (int k = 0; k < BK / 16; ++k) {
-                                const uint64_t ad = sw128_kmajor_desc(ac + k * 32);
-                                mma_bf16(d, ad, sw128_kmajor_desc(bg + k * 32), IDESC_H, (kb | c | k) != 0);
-                                mma_bf16(d + BN / 2, ad, sw128_kmajor_desc(bu + k * 32), IDESC_H, (kb | c | k) != 0);
-                            }
-                        } else {
-                            const uint32_t bc = b0 + c * B_SUB;
+                        for (int c = 0; c < KC; ++c)
+                            if (c < nc)
 #pragma unroll
-                            for (int k = 0; k < BK / 16; ++k)
-                                mma_bf16(d, sw128_kmajor_desc(ac + k * 32), sw128_kmajor_desc(bc + k * 32), IDESC,
-                                         (kb | c | k) != 0);
+                                for (int k = 0; k < BK / 16; ++k)
+                                    mma_bf16(d + half * (BN / 2), sw128_kmajor_desc(a0 + c * A_SUB + k * 32),
+                                             sw128_kmajor_desc(b0 + c * H_SUB + k * 32), IDESC, (kb | c | k) != 0);
+                        mma_commit(&S->bempty[bs]);
+                        if (half == 1) {
+                            mma_commit(&S->empty[stage]);
+                            if (kb == num_kb - 1) mma_commit(&S->accf[acc]);
                         }
                     }
-                    mma_commit(&S->empty[stage]);
-                    if (++stage == STAGES) { stage = 0; phase ^= 1; }
+                    __syncwarp();
+                    if (++bs == BSLOTS) { bs = 0; bphase ^= 1; }
                 }
                 if (!ok) break;
-                mma_commit(&S->accf[acc]);
-                if (++acc == 2) { acc = 0; aphase ^= 1; }
+                if (++stage == STAGES) { stage = 0; phase ^= 1; }
             }
-            if (!ok) record_status(g.status, MOE_ERR_TIMEOUT);
-            // TMEM may only be released once every MMA issued here has completed
-            mma_commit(&S->fin);
-            if (!mbar_wait(&S->fin, 0)) record_status(g.status, MOE_ERR_TIMEOUT);
+            if (!ok) break;
+            if (++acc == 2) { acc = 0; aphase ^= 1; }
         }
+        // TMEM may only be released once every MMA issued here has completed
+        if (elect_one()) mma_commit(&S->fin);
+        __syncwarp();
+        if (!warp_wait(&S->fin, 0)) ok = false;
+        if (!ok && lane == 0) record_status(g.status, MOE_ERR_TIMEOUT);
         __syncwarp();
     } else {
         // ------------------------------------------------------------ epilogue

@@ -506,7 +506,7 @@ moe_status_t forward_bf16(const moe_dims_t *d, const void *x, const void *router
         !encode_4d_chunked(&tm_wg, w_gate, d->E, d->I, d->H, 128, 2) ||
         !encode_4d_chunked(&tm_wu, w_up, d->E, d->I, d->H, 128, 2) ||
         !moe::encode_a_maps(&tm_h, h, R, d->I, false) ||
-        !encode_4d_chunked(&tm_wd, w_down, d->E, d->H, d->I, pairs ? 128 : 256, 2))
+        !encode_4d_chunked(&tm_wd, w_down, d->E, d->H, d->I, 128, 2))
         return MOE_ERR_CUDA;
     // the shared expert: x itself as its gate/up A operand, its weights as chunked maps
     // with the boxes of the routed experts' maps
@@ -514,7 +514,7 @@ moe_status_t forward_bf16(const moe_dims_t *d, const void *x, const void *router
     if (sh && (!moe::encode_a_maps(&sm1.x, x, d->T, d->H, false) ||
                !moe::encode_sw128_chunked_bf16(&sm1.b0, shared_gate, shared_I, d->H, 128, 2) ||
                !moe::encode_sw128_chunked_bf16(&sm1.b1, shared_up, shared_I, d->H, 128, 2) ||
-               !moe::encode_sw128_chunked_bf16(&sm2.b0, shared_down, d->H, shared_I, pairs ? 128 : 256, 2)))
+               !moe::encode_sw128_chunked_bf16(&sm2.b0, shared_down, d->H, shared_I, 128, 2)))
         return MOE_ERR_CUDA;
     // gate/up A rows straight from x: one-row boxes for tile::gather4, the token of
     // sorted row r being sorted_to_flat[r] / k
