@@ -109,6 +109,66 @@ def test_against_64_bits(T, H, I, E, k, empty):
     assert bool((out[:T][gone] == 0).all())
 
 
+# lists on both sides of what one block groups (4096 entries, 376 experts), tiles whose last rows fill part of a warp, and
+# groups of hundreds of rows
+MORE = [(512, 128, 64, 16, 8), (513, 128, 64, 16, 8), (300, 64, 64, 376, 3), (300, 64, 64, 377, 3), (400, 192, 320, 4, 4),
+        (700, 256, 64, 3, 3), (1, 2048, 512, 64, 6), (95, 64, 64, 1, 1), (3100, 64, 192, 4, 1)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,H,I,E,k", MORE)
+@pytest.mark.parametrize("skew", [False, True])
+def test_groups_of_any_size(T, H, I, E, k, skew):
+    x, W = rnd((T, H), 1), weights(E, H, I)
+    idx, w = routing(T, E, k, empty=0.1)
+    if skew:  # most rows with one expert
+        hot = torch.rand(T, k, generator=torch.Generator().manual_seed(8)).cuda() < 0.8
+        idx[hot & (idx >= 0)] = E // 2
+    ws = api.experts_workspace(T, H, I, E, k, "cuda").fill_(0x7F)
+    out = api.moe_experts(x, idx, w, *W, ws=ws)
+    assert api.moe_get_device_status(ws) == api.MOE_OK
+    check(out, x, idx, w, *W)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 17, 130, 600])
+def test_a_chain_of_launches_sees_what_the_last_one_wrote(T):
+    """Routing and experts on one workspace, one after the other with nothing between: each call's
+    experts take the routing of the call just before."""
+    H, I, E, k, n = 256, 128, 32, 4, 6
+    W = weights(E, H, I)
+    xs, logits = [rnd((T, H), 30 + i) for i in range(n)], [rnd((T, E), 40 + i, 2.0, torch.float32) for i in range(n)]
+    ws = api.experts_workspace(T, H, I, E, k, "cuda")
+    idx, w = torch.zeros(T, k, dtype=torch.int32, device="cuda"), torch.zeros(T, k, device="cuda")
+
+    def chain():
+        outs = []
+        for x, l in zip(xs, logits):
+            api.moe_route_scored(l, k, topk_idx=idx, topk_w=w)
+            outs.append(api.moe_experts(x, idx, w, *W, ws=ws))
+        return outs
+
+    want = []
+    for x, l in zip(xs, logits):
+        i, v = api.moe_route_scored(l, k)
+        torch.cuda.synchronize()
+        want.append(api.moe_experts(x, i, v, *W))
+        torch.cuda.synchronize()
+        check(want[-1], x, i, v, *W)
+    for _ in range(3):
+        for a, b in zip(chain(), want):
+            assert torch.equal(a, b)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = chain()
+    for _ in range(3):
+        for o in outs:
+            o.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("T", [20, 400])
 def test_kernel_choices_agree(T):

@@ -167,6 +167,50 @@ def test_strides_in_place_and_rows_behind(M, N, K):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K", [(257, 4104, 200), (1500, 1000, 136), (2600, 2056, 72), (3001, 520, 1100), (129, 2048, 2048)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rows_and_columns_behind_aligned_outputs(M, N, K, dtype):
+    # rows of out 16-byte aligned, M and N not multiples of any tile: nothing behind either is written
+    x, w, u = operands(M, N, K)
+    b = mat(1, N, 4, dtype=torch.float32)[0]
+    for pad in (0, 8, 24):
+        for gate, act in ((None, "gelu"), (u, "silu")):
+            out = torch.full((M + 3, N + pad), 7.0, dtype=dtype, device="cuda")
+            check(x, w, b, act, mat(M, N, 8, 16, dtype), gate, out_dtype=dtype, out=out[:M, :N])
+            assert bool((out[M:] == 7.0).all()) and bool((out[:, N:] == 7.0).all())
+            check(x, w, None, act, None, gate, out_dtype=dtype, out=out[:M, :N])
+            assert bool((out[M:] == 7.0).all()) and bool((out[:, N:] == 7.0).all())
+            res = mat(M, N, 9, pad, dtype).clone()
+            check(x, w, b, act, res, gate, out_dtype=dtype, out=res)     # onto the residual
+    # one of the two not aligned
+    out = torch.empty(M, N + 8, dtype=dtype, device="cuda")
+    check(x, w, b, "relu", mat(M, N, 8, 3, dtype), out_dtype=dtype, out=out[:, :N])
+    check(x, w, b, "relu", mat(M, N, 8, 8, dtype), out_dtype=dtype, out=out[:, 1:N + 1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", list(api.ACTS))
+@pytest.mark.parametrize("M", [5, 200, 2000])
+def test_activations_of_extreme_values(act, M):
+    # as the formula in 64 bits has them, NaN where that is NaN
+    v = torch.tensor([0.0, -0.0, 1e-30, -1e-30, 1e-42, 3e4, -3e4, 1e20, -1e20, 3e38, -3e38, math.inf, -math.inf, math.nan, 88.0, -88.0,
+                      -103.0, 13.0, -13.0], device="cuda")
+    N = 512
+    b = v.repeat(N // v.numel() + 1)[:N].contiguous()
+    x, w = torch.zeros(M, 64, device="cuda").bfloat16(), torch.zeros(N, 64, device="cuda").bfloat16()
+    got = api.moe_linear(x, w, b, act, out_dtype=torch.float32)
+    want = act64(b.double(), act)
+    if act == "gelu_tanh":  # 1 + tanh loses all it has left of 64 bits below -5; the same formula by exp keeps it
+        z = 2.0 * math.sqrt(2.0 / math.pi) * (b.double() + 0.044715 * b.double() ** 3)
+        want = torch.where(b < 0, b.double() * torch.exp(z) / (1.0 + torch.exp(z)), want)
+    # a relative error that grows with the exponent (up to 6 roundings of an argument of up to 104), and
+    # what fp32 cannot hold
+    tol = (12.0 + 6.0 * 104.0) * 2.0 ** -24 * want.abs() + 2.0 ** -125
+    same = (got.double() == want) | (torch.isnan(want) & torch.isnan(got)) | ((got.double() - want).abs() <= tol)
+    assert bool(same.all()), [(float(b[i]), float(got[j, i]), float(want[i])) for j, i in (~same).nonzero()[:5].tolist()]
+
+
+@pytest.mark.gpu
 def test_what_lies_outside_the_operands_is_not_read_into_the_sums():
     # NaN behind the rows, columns and depth of every operand
     for M, N, K in ((5, 70, 72), (130, 200, 100), (1030, 600, 136), (2570, 2100, 100)):
