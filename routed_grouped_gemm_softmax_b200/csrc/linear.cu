@@ -7,12 +7,11 @@
 //
 // linear_kernel: 128 rows of w (gated: 64 of w over 64 of w_up) on the MMA's M side and BN
 // rows of x on its N side, so that the tensor work of a short batch follows its rows.  A
-// tile's K range is split over the S CTAs of a cluster; each leaves its fp32 partial tile in
-// its own shared memory, and every CTA then sums its share of the tile's rows over the S
-// partials (in rank order, through distributed shared memory) and finishes them.
-// With at most half an SM's shared memory a CTA, two are resident per SM: 33 clusters of 8
-// fit on the GPU, where one CTA an SM leaves room for 15 (the GPCs' SMs do not divide by
-// 8) and 16 x (2 x 2048) x 7168 ran in two waves, 22.9 us.
+// tile's K range is split over the S CTAs of a cluster; each copies to every CTA the rows of
+// its fp32 partial tile that this one finishes, which sums them in rank order.
+// Bound by latency, not by the weight stream, while that is short: of the 3.6 us of
+// 1 x 2048 x 2048 (1.3 at the memory's rate) 0.5 are the first load, 0.5 to 1 the tensor core's
+// results, 1 the exchange and the epilogue, the rest the launch.  16 x 4096 x 4096 8.9 us (5.2).
 // linear_pair.cu takes the batches with enough rows to be bound by the tensor cores.
 #include <mutex>
 
@@ -433,12 +432,13 @@ cudaError_t launch_pairs(const moe_linear_t &d, const void *x, const void *w, co
     return launch_linear_pair(maps, g, g.gated, nb, st);
 }
 
-// The kernel and tile of a call.  Up to 128 rows the narrowest tile that holds them (4096 x 4096
-// in us: 16 rows 10.7 on tiles of 16, 11.1 of 32, 13.9 of 128; 64 rows 12.6 of 64, 16.8 of 32, 15.1 of
-// 128).  Above, CTA pairs once their 256 x 128 tiles occupy 64 SMs (4096 x 256 x 2048: 15.0 on 32 of
-// them, 16.2 to 17.8 on linear_kernel's; 300 x 1000 x 1000, 16 tiles: 12.0 against 8.1).  A stage of a
-// 256 x 256 tile takes half as long again as one of a 256 x 128 tile, and the tiles run in waves of
-// all pairs: 512 x 4096 x 4096 22.4 on 64 tiles of 128, 30.6 on 32 of 256; 1024 rows 37.5 and 31.4.
+// The kernel and tile of a call.  The narrowest tile that holds the rows, of 16, 32 or 64 (x 4096 x
+// 4096, us: 16 rows 8.9 on tiles of 16, 8.9 of 32, 9.3 of 64; 64 rows 14.3, 10.3, 10.1).  Above 128
+// rows CTA pairs once their 256 x 128 tiles occupy 64 SMs (600 x 2048 x 512, 48 tiles: 6.4 on
+// them, 10.4 on linear_kernel's; 512 x 2048 x 2048, 32 tiles: 10.8 and 10.5; 300 x 1000 x 1000, 16
+// tiles: 9.2 and 6.2).  A stage of a 256 x 256 tile takes half as long again as one of a 256 x
+// 128 tile, and the tiles run in waves of all pairs: 512 x 4096 x 4096 17.8 on 64 tiles of 128, 25.7
+// on 32 of 256; 1024 rows 30.0 and 27.4; 1500 x 4104 x 1408, 3 waves and 2, 18.1 and 20.5.
 cudaError_t launch_linear(const moe_linear_t &d, const void *x, const void *w, const void *w_up, const LinArgs &g,
                           cudaStream_t st)
 {
@@ -449,7 +449,7 @@ cudaError_t launch_linear(const moe_linear_t &d, const void *x, const void *w, c
     };
     if (d.M > 128 && tiles(128) >= 32) {
         const long long w128 = (tiles(128) + pairs - 1) / pairs, w256 = (tiles(256) + pairs - 1) / pairs;
-        return launch_pairs(d, x, w, w_up, g, !g.promote && 3 * w256 <= 2 * w128 ? 256 : 128, st);
+        return launch_pairs(d, x, w, w_up, g, !g.promote && 3 * w256 < 2 * w128 ? 256 : 128, st);
     }
     if (d.M <= 16) return launch_split<16>(d, x, w, w_up, g, st);
     if (d.M <= 32) return launch_split<32>(d, x, w, w_up, g, st);
