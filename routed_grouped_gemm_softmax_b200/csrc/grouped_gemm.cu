@@ -54,7 +54,7 @@ constexpr int BM = kTileRows;  // 128 rows per tile
 constexpr int BK = 64;         // a K chunk: 64 bf16 = one 128-byte swizzle row
 constexpr int KC = 2;          // K chunks per stage
 constexpr int BKS = BK * KC;   // K of a stage: 128
-constexpr int BN = 256;        // output columns per item (gate/up: 128 + 128)
+constexpr int BN = 256;        // columns of an accumulator: two halves of up to 128
 // Stages of 128 K columns: each weight box then brings both chunks of its rows, 256
 // contiguous bytes a row, which DRAM streams about a third faster than 128-byte row
 // pieces.  A stage's A rows and the two halves of its B rows (gate and up, or 128 + 128
@@ -62,22 +62,25 @@ constexpr int BN = 256;        // output columns per item (gate/up: 128 + 128)
 // is multiplied (1024 tokens, k 4 of 64 experts: the call 98.8 us with one barrier for
 // the 96 KB of a stage, 93.6 so; 16 tokens, k 8 of 256: 77.0 and 75.0).  The finer steps need
 // converged producer and MMA warps: by lane 0 alone they were slower, 99.9 us.
-constexpr int STAGES = 2;       // A slots
-constexpr int BSLOTS = 4;       // B half slots
+//
+// A half is BH = 128 rows of B.  Batches with too few items of that width to occupy the GPU
+// take halves of 64 or 32 (moe_experts: one token, k 6 of 64 experts, H 2048, I 512: 24 gate/up
+// items of 128, 96 of 32), in more and smaller slots.
+__host__ __device__ constexpr int stages_of(int BH) { return BH == 128 ? 2 : BH == 64 ? 3 : 4; }  // A slots
+constexpr int STAGES_MAX = 4, BSLOTS_MAX = 8;
 constexpr int RING = 4;
 constexpr int A_SUB = BM * BK * 2;     // 16 KB: one chunk of A rows
-constexpr int B_SUB = BN * BK * 2;     // 32 KB: one chunk of B rows
 constexpr int A_BYTES = A_SUB * KC;    // 32 KB
-constexpr int H_SUB = B_SUB / 2;       // 16 KB: one chunk of half the B rows
-constexpr int H_BYTES = H_SUB * KC;    // 32 KB
+__host__ __device__ constexpr int h_sub(int BH) { return BH * BK * 2; }       // one chunk of half the B rows
+__host__ __device__ constexpr int h_bytes(int BH) { return h_sub(BH) * KC; }  // 32 KB of 128
 constexpr int THREADS = 192;
 constexpr uint32_t TMEM_COLS = 512;   // two 128 x 256 fp32 accumulators
 
 struct Ctrl {
-    uint64_t full[STAGES];   // TMA bytes landed in A slot s
-    uint64_t empty[STAGES];  // MMAs reading A slot s finished
-    uint64_t bfull[BSLOTS];  // the same of B slot s
-    uint64_t bempty[BSLOTS];
+    uint64_t full[STAGES_MAX];   // TMA bytes landed in A slot s
+    uint64_t empty[STAGES_MAX];  // MMAs reading A slot s finished
+    uint64_t bfull[BSLOTS_MAX];  // the same of B slot s
+    uint64_t bempty[BSLOTS_MAX];
     uint64_t accf[2];        // accumulator a holds a finished tile
     uint64_t acce[2];        // epilogue drained accumulator a
     uint64_t itf[RING];      // ring slot r holds the next item id
@@ -89,7 +92,10 @@ struct Ctrl {
 };
 
 constexpr size_t CTRL_BYTES = (sizeof(Ctrl) + 127) / 128 * 128;
-constexpr size_t SMEM_BYTES = 1024 + (size_t)STAGES * A_BYTES + (size_t)BSLOTS * H_BYTES + CTRL_BYTES;
+constexpr size_t smem_bytes(int BH)
+{
+    return 1024 + (size_t)stages_of(BH) * (A_BYTES + 2 * h_bytes(BH)) + CTRL_BYTES;
+}
 
 __device__ __forceinline__ void record_status(int32_t *status, int code) { atomicCAS(status, 0, code); }
 
@@ -126,15 +132,16 @@ __device__ __forceinline__ bool wait_count_at_least(const int32_t *ctr, int targ
 
 __device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
 
-template <int MODE>
+template <int MODE, int BH>
 __global__ void __launch_bounds__(THREADS, 1)
 grouped_gemm_kernel(const __grid_constant__ AMaps tmA, const __grid_constant__ CUtensorMap tmB0,
                     const __grid_constant__ CUtensorMap tmB1, const GemmArgs g, const __grid_constant__ SharedMaps sm,
                     const __grid_constant__ LayerMaps lm)
 {
-    // Output columns per tile: the gate/up items pack 128 gate + 128 up columns into
-    // N=256; the down (and dense) items write 256 columns.
-    constexpr int BNO0 = BN / 2, BNO1 = BN;
+    // Output columns per tile: the gate/up items take BH gate and the same BH up columns; the
+    // down items write 2 BH columns.
+    constexpr int BNO0 = BH, BNO1 = 2 * BH;
+    constexpr int STAGES = stages_of(BH), BSLOTS = 2 * STAGES, H_SUB = h_sub(BH), H_BYTES = h_bytes(BH);
     const bool dense = g.tiles == nullptr;  // mode 2: m-tiles are plain 128-row blocks of A
     extern __shared__ uint8_t smem_raw[];
     const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
@@ -326,7 +333,7 @@ grouped_gemm_kernel(const __grid_constant__ AMaps tmA, const __grid_constant__ C
                     // n0 + 128 half..: the expert's, or chunks of columns s*I.. of the shared down
                     const CUtensorMap *bm = !p1 ? half ? &tmB1 : &tmB0 : MODE == 3 ? &lm.wd : &tmB0;
                     const CUtensorMap *bsh = !p1 ? half ? &sm.b1 : &sm.b0 : MODE == 3 ? &lm.wd_sh : &sm.b0;
-                    const int brow = p1 ? n0 + half * (BN / 2) : n0;
+                    const int brow = p1 ? n0 + half * BH : n0;
                     if (elect_one()) {
                         mbar_arrive_expect_tx(bar, H_BYTES);
                         if (tr.s < 0)
@@ -378,7 +385,7 @@ grouped_gemm_kernel(const __grid_constant__ AMaps tmA, const __grid_constant__ C
     } else if (warp == 1) {
         // ---------------------------------------------------------- MMA issuer
         // (the whole warp, converged: warp_ptx.cuh)
-        constexpr uint32_t IDESC = idesc_bf16_f32(BM, BN / 2);  // gate, up, or 128 down columns
+        constexpr uint32_t IDESC = idesc_bf16_f32(BM, BH);  // gate, up, or BH down columns
         const uint32_t sA0 = smem_u32(sA), sB0 = smem_u32(sB);
         int stage = 0, bs = 0, rs = 0, acc = 0;
         uint32_t phase = 0, bphase = 0, rphase = 0, aphase = 0;
@@ -472,7 +479,7 @@ grouped_gemm_kernel(const __grid_constant__ AMaps tmA, const __grid_constant__ C
                 for (int c = 0; c < BNO0 / 32; ++c) {
                     uint32_t gr[32], ur[32];
                     tmem_ld32_sync(tb + c * 32, gr);
-                    tmem_ld32_sync(tb + BNO0 + c * 32, ur);
+                    tmem_ld32_sync(tb + BN / 2 + c * 32, ur);
                     const int col = nt * BNO0 + c * 32;
                     if (mine > 0 && col < g.N) {
                         uint32_t pk[16];
@@ -512,7 +519,7 @@ grouped_gemm_kernel(const __grid_constant__ AMaps tmA, const __grid_constant__ C
 #pragma unroll 1
                 for (int c = 0; c < BNO1 / 32; ++c) {
                     uint32_t r[32];
-                    tmem_ld32_sync(tb + c * 32, r);
+                    tmem_ld32_sync(tb + (c * 32 < BH ? 0 : BN / 2 - BH) + c * 32, r);
                     const int col = nt * BNO1 + c * 32;
                     if (mine <= 0) continue;
                     if (col < N && g.y_f32) {
@@ -571,42 +578,46 @@ int num_sms()
 
 // The kernels need more than the default 48 KB of dynamic shared memory; the
 // attribute is set once per device (and per kernel) rather than on every launch.
-static bool smem_attr_ready(int mode)
+template <int MODE, int BH>
+static cudaError_t launch_mode(const GemmArgs &g, const AMaps &tmA, const CUtensorMap &tmB0, const CUtensorMap &tmB1,
+                               const SharedMaps &s, const LayerMaps &l, cudaStream_t st)
 {
     static std::mutex mu;
-    static uint64_t done[4] = {0, 0, 0, 0};  // bit per device
+    static uint64_t done = 0;  // bit per device
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
-    std::lock_guard<std::mutex> lk(mu);
-    if (done[mode] >> dev & 1ull) return true;
-    const int a = (int)SMEM_BYTES + 4 * kRowStoreBytes;
-    if (mode == 2) return false;  // no dense mode: the router's tensor-core logits run in the fp8 kernel
-    cudaError_t e = mode == 0   ? cudaFuncSetAttribute(grouped_gemm_kernel<0>, cudaFuncAttributeMaxDynamicSharedMemorySize, a)
-                  : mode == 1 ? cudaFuncSetAttribute(grouped_gemm_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, a)
-                              : cudaFuncSetAttribute(grouped_gemm_kernel<3>, cudaFuncAttributeMaxDynamicSharedMemorySize, a);
-    if (e != cudaSuccess) return false;
-    done[mode] |= 1ull << dev;
-    return true;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidValue;
+    {
+        std::lock_guard<std::mutex> lk(mu);
+        if (!(done >> dev & 1ull)) {
+            const int a = (int)smem_bytes(BH) + 4 * kRowStoreBytes;
+            if (cudaFuncSetAttribute(grouped_gemm_kernel<MODE, BH>, cudaFuncAttributeMaxDynamicSharedMemorySize, a) !=
+                cudaSuccess)
+                return cudaErrorInvalidValue;
+            done |= 1ull << dev;
+        }
+    }
+    const int grid = g.ctas > 0 ? g.ctas : num_sms();
+    const size_t smem = smem_bytes(BH) + (g.turn_rows ? 4 * kRowStoreBytes : 0);
+    return launch_pdl(grouped_gemm_kernel<MODE, BH>, dim3(grid), dim3(THREADS), smem, st, tmA, tmB0, tmB1, g, s, l);
 }
 
 cudaError_t launch_grouped_gemm(const GemmArgs &g, const AMaps &tmA, const CUtensorMap &tmB0,
                                 const CUtensorMap &tmB1, cudaStream_t st, const SharedMaps *sm, const LayerMaps *lm)
 {
-    const int grid = g.ctas > 0 ? g.ctas : num_sms();
-    if (g.mode < 0 || g.mode > 3 || g.mode == 2 || !smem_attr_ready(g.mode)) return cudaErrorInvalidValue;
-    if (g.sh_count && (!sm || g.mode == 2)) return cudaErrorInvalidValue;
+    if (g.mode < 0 || g.mode > 3 || g.mode == 2) return cudaErrorInvalidValue;  // no dense mode here: it is fp8.cu's
+    if (g.sh_count && !sm) return cudaErrorInvalidValue;
     if (g.mode == 3 && (!lm || !g.ready)) return cudaErrorInvalidValue;
+    if (g.half_rows && (g.mode != 3 || g.comb_cnt || g.sh_count)) return cudaErrorInvalidValue;
     if (g.a_rows && (!sm || g.a_div <= 0 || g.a_tokens <= 0 || (g.mode != 0 && g.mode != 3))) return cudaErrorInvalidValue;
     static const SharedMaps none{};
     static const LayerMaps nolm{};
     const SharedMaps &s = sm ? *sm : none;
     const LayerMaps &l = lm ? *lm : nolm;
-    const size_t smem = SMEM_BYTES + (g.turn_rows ? 4 * kRowStoreBytes : 0);
-    switch (g.mode) {
-    case 0: return launch_pdl(grouped_gemm_kernel<0>, dim3(grid), dim3(THREADS), smem, st, tmA, tmB0, tmB1, g, s, l);
-    case 1: return launch_pdl(grouped_gemm_kernel<1>, dim3(grid), dim3(THREADS), smem, st, tmA, tmB0, tmB1, g, s, l);
-    default: return launch_pdl(grouped_gemm_kernel<3>, dim3(grid), dim3(THREADS), smem, st, tmA, tmB0, tmB1, g, s, l);
-    }
+    if (g.mode == 0) return launch_mode<0, 128>(g, tmA, tmB0, tmB1, s, l, st);
+    if (g.mode == 1) return launch_mode<1, 128>(g, tmA, tmB0, tmB1, s, l, st);
+    if (g.half_rows == 32) return launch_mode<3, 32>(g, tmA, tmB0, tmB1, s, l, st);
+    if (g.half_rows == 64) return launch_mode<3, 64>(g, tmA, tmB0, tmB1, s, l, st);
+    return launch_mode<3, 128>(g, tmA, tmB0, tmB1, s, l, st);
 }
 
 }  // namespace moe

@@ -237,6 +237,7 @@ struct GemmArgs {
     float *y_f32;
     // Full warps of h and y rows are turned in shared memory before they are stored (row_store.cuh).
     bool turn_rows;
+    int half_rows;  // mode 3: 32 or 64 rows of gate and of up an item (the maps' boxes), or 0: 128
 };
 
 // Tensor maps of the down half of the fused layer GEMM (mode 3): h as its A operand
