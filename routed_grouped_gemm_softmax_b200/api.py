@@ -269,7 +269,8 @@ def moe_route_scored(logits, top_k: int, scoring: str = "softmax", bias=None, n_
     else:
         _need_on(topk_idx, dev, torch.int32, (T, top_k), "topk_idx")
     if topk_w is None:
-        topk_w = _empty((T, top_k), torch.float32, logits, stream)
+        topk_w = (torch.empty_like(topk_idx, dtype=torch.float32) if stream is None else
+                  _empty((T, top_k), torch.float32, topk_idx, stream))
     else:
         _need_on(topk_w, dev, torch.float32, (T, top_k), "topk_w")
     o = Scored(T, E, top_k, SCORINGS[scoring], n_groups, topk_groups, GROUP_SCORES[group_score], bool(renormalize),

@@ -512,12 +512,14 @@ moe_status_t forward_bf16(const moe_dims_t *d, const void *x, const void *router
         const int64_t tiles = (A < d->E ? A : d->E) + A / moe::kTileRows;
         while (half > 32 && 4 * tiles * ((d->I + half - 1) / half) < 3 * moe::num_sms()) half /= 2;
     }
-    if (!moe::encode_a_maps(&tm_xs, xs, A, d->H, false) ||
+    const bool direct = plan & MOE_PLAN_DIRECT_A;
+    if (!moe::encode_a_maps(&tm_h, h, R, d->I, false) ||
+        (!direct && !moe::encode_a_maps(&tm_xs, xs, A, d->H, false)) ||
         !encode_4d_chunked(&tm_wg, w_gate, d->E, d->I, d->H, half, 2) ||
         !encode_4d_chunked(&tm_wu, w_up, d->E, d->I, d->H, half, 2) ||
-        !moe::encode_a_maps(&tm_h, h, R, d->I, false) ||
         !encode_4d_chunked(&tm_wd, w_down, d->E, d->H, d->I, half, 2))
         return MOE_ERR_CUDA;
+    if (direct) tm_xs = tm_h;  // no sorted copy: not loaded through
     // the shared expert: x itself as its gate/up A operand, its weights as chunked maps
     // with the boxes of the routed experts' maps
     moe::SharedMaps sm1{}, sm2{};
@@ -528,7 +530,6 @@ moe_status_t forward_bf16(const moe_dims_t *d, const void *x, const void *router
         return MOE_ERR_CUDA;
     // gate/up A rows straight from x: one-row boxes for tile::gather4, the token of
     // sorted row r being sorted_to_flat[r] / k
-    const bool direct = plan & MOE_PLAN_DIRECT_A;
     if (direct && !encode_2d(&sm1.xg, x, d->T, d->H, 1)) return MOE_ERR_CUDA;
     // the tile list is then the output of the kernel just before the gate/up GEMM
     // when the router and the grouping, or the whole grouping, are one launch
