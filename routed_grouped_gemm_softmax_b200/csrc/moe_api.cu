@@ -439,25 +439,25 @@ cudaError_t group_assignments(const moe_dims_t &d, const moe::WsLayout &L, const
                               const StageMarks &marks, cudaStream_t st)
 {
     cudaError_t e = cudaSuccess;
-    if (given && moe::permute_one_ok(d)) {  // no fused combine: its counts are not read
+    if (given) {  // no fused combine: its counts are not read
         e = marks.mark(1, st);
         if (e != cudaSuccess) return e;
-        return moe::launch_permute_one(d, given->idx, at<int32_t>(ws, L.offsets), at<int32_t>(ws, L.s2f),
-                                       at<int32_t>(ws, L.f2s), at<int32_t>(ws, L.tiles), at<int32_t>(ws, L.ntiles),
-                                       at<int32_t>(ws, L.tiles2), at<int32_t>(ws, L.ntiles2), hdr,
-                                       at<int32_t>(ws, L.ready), (int)((L.clear_bytes - L.ready) / 4), st, true);
+        const int nready = (int)((L.clear_bytes - L.ready) / 4);
+        if (moe::permute_one_ok(d))
+            return moe::launch_permute_one(d, given->idx, at<int32_t>(ws, L.offsets), at<int32_t>(ws, L.s2f),
+                                           at<int32_t>(ws, L.f2s), at<int32_t>(ws, L.tiles), at<int32_t>(ws, L.ntiles),
+                                           at<int32_t>(ws, L.tiles2), at<int32_t>(ws, L.ntiles2), hdr,
+                                           at<int32_t>(ws, L.ready), nready, st, true);
+        return moe::launch_permute(d, L, given->idx, at<int32_t>(ws, L.blk_cnt), at<int32_t>(ws, L.blk_base),
+                                   at<int32_t>(ws, L.offsets), at<int32_t>(ws, L.s2f), at<int32_t>(ws, L.f2s),
+                                   at<int32_t>(ws, L.tiles), at<int32_t>(ws, L.ntiles), hdr, st,
+                                   at<int32_t>(ws, L.tiles2), at<int32_t>(ws, L.ntiles2), true,
+                                   at<int32_t>(ws, L.ready), nready);
     }
-    if (given || !moe::small_route_permute_ok(d))  // else the router's kernels clear them
+    if (!moe::small_route_permute_ok(d))  // else the router's kernels clear them
         e = cudaMemsetAsync(hdr, 0, L.clear_bytes, st);
     if (e != cudaSuccess) return e;
-    if (!given) return route_and_permute(d, L, x, router_w, router_bias, ws, hdr, marks, st);
-    e = marks.mark(1, st);
-    if (e == cudaSuccess)
-        e = moe::launch_permute(d, L, given->idx, at<int32_t>(ws, L.blk_cnt), at<int32_t>(ws, L.blk_base),
-                                at<int32_t>(ws, L.offsets), at<int32_t>(ws, L.s2f), at<int32_t>(ws, L.f2s),
-                                at<int32_t>(ws, L.tiles), at<int32_t>(ws, L.ntiles), hdr, st, at<int32_t>(ws, L.tiles2),
-                                at<int32_t>(ws, L.ntiles2), true);
-    return e;
+    return route_and_permute(d, L, x, router_w, router_bias, ws, hdr, marks, st);
 }
 
 // The bf16 layer.  `given` null: routed by x and router_w; else on that routing, router_w

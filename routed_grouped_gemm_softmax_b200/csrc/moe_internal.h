@@ -144,11 +144,13 @@ cudaError_t launch_route_permute_small(const moe_dims_t &d, const __nv_bfloat16 
 // Also writes the 2 x 128-row pair tiles when tiles2 is non-null.  none_ok: entries of -1
 // are assignments to no expert, skipped without an error; f2s of every skipped entry
 // is -1 (else it is left as it was); s2f past the last sorted row is 0.
+// With `ready` the kernels clear the header and the `nready` counts there first (a memset before
+// them would end the overlap of their launches: 2048 tokens, k 8 of 64 experts, H 1024, 133 us a call, 127 so).
 cudaError_t launch_permute(const moe_dims_t &d, const WsLayout &L, const int32_t *idx,
                            int32_t *blk_cnt, int32_t *blk_base, int32_t *offsets, int32_t *s2f,
                            int32_t *f2s, int32_t *tiles, int32_t *ntiles, WsHeader *hdr,
                            cudaStream_t st, int32_t *tiles2 = nullptr, int32_t *ntiles2 = nullptr,
-                           bool none_ok = false);
+                           bool none_ok = false, int32_t *ready = nullptr, int nready = 0);
 
 // The same by one block, which clears the header and the `nready` counts at `ready` first: for lists
 // of up to kPermOneMaxA entries (4 steps a warp: 12288 took 21 us against 16 of a memset and the

@@ -26,12 +26,19 @@ __device__ __forceinline__ void record_status(int32_t *status, int code)
     if (status) atomicCAS(status, 0, code);
 }
 
+// With `hdr` the first block clears the header and the `nready` counts at `ready`, and bad indices are
+// left to the scatter kernel to record.
 __global__ void perm_count_kernel(const int32_t *__restrict__ idx, int A, int E, int chunk,
-                                  int32_t *__restrict__ blk_cnt, int32_t *status, int none_ok)
+                                  int32_t *__restrict__ blk_cnt, int32_t *status, int none_ok, WsHeader *hdr,
+                                  int32_t *ready, int nready)
 {
     pdl_wait();
     pdl_trigger();
     extern __shared__ int hist[];
+    if (hdr && blockIdx.x == 0) {
+        if (threadIdx.x < 8) threadIdx.x ? hdr->counter[threadIdx.x - 1] = 0 : hdr->status = 0;
+        for (int i = threadIdx.x; i < nready; i += blockDim.x) ready[i] = 0;
+    }
     for (int e = threadIdx.x; e < E; e += blockDim.x) hist[e] = 0;
     __syncthreads();
     const int f0 = blockIdx.x * chunk;
@@ -40,7 +47,7 @@ __global__ void perm_count_kernel(const int32_t *__restrict__ idx, int A, int E,
         const int e = idx[f];
         if (e >= 0 && e < E)
             atomicAdd(&hist[e], 1);
-        else if (!(none_ok && e == -1))
+        else if (!hdr && !(none_ok && e == -1))
             record_status(status, MOE_ERR_BAD_INDEX);
     }
     __syncthreads();
@@ -130,7 +137,8 @@ perm_scan_kernel(int E, int nb, const int32_t *__restrict__ blk_cnt, int32_t *__
 
 __global__ void perm_scatter_kernel(const int32_t *__restrict__ idx, int A, int E,
                                     const int32_t *__restrict__ blk_base, int32_t *__restrict__ s2f,
-                                    int32_t *__restrict__ f2s, int none_ok, const int32_t *__restrict__ offsets)
+                                    int32_t *__restrict__ f2s, int none_ok, const int32_t *__restrict__ offsets,
+                                    int32_t *status)
 {
     pdl_wait();
     pdl_trigger();
@@ -151,6 +159,7 @@ __global__ void perm_scatter_kernel(const int32_t *__restrict__ idx, int A, int 
     __syncthreads();
     if (!valid) {
         if (none_ok && f < A) f2s[f] = -1;
+        if (status && f < A && !(none_ok && e == -1)) record_status(status, MOE_ERR_BAD_INDEX);
         return;
     }
     int prior = 0;
@@ -273,17 +282,19 @@ __global__ void gather_rows_kernel(const __nv_bfloat16 *__restrict__ x,
 cudaError_t launch_permute(const moe_dims_t &d, const WsLayout &L, const int32_t *idx,
                            int32_t *blk_cnt, int32_t *blk_base, int32_t *offsets, int32_t *s2f,
                            int32_t *f2s, int32_t *tiles, int32_t *ntiles, WsHeader *hdr,
-                           cudaStream_t st, int32_t *tiles2, int32_t *ntiles2, bool none_ok)
+                           cudaStream_t st, int32_t *tiles2, int32_t *ntiles2, bool none_ok, int32_t *ready,
+                           int nready)
 {
     const int A = d.T * d.top_k, E = d.E;
     cudaError_t e = launch_pdl(perm_count_kernel, dim3(L.nb), dim3(256), E * sizeof(int), st, idx, A, E, L.chunk,
-                               blk_cnt, hdr ? &hdr->status : nullptr, (int)none_ok);
+                               blk_cnt, hdr ? &hdr->status : nullptr, (int)none_ok, ready ? hdr : nullptr, ready,
+                               nready);
     if (e == cudaSuccess)
         e = launch_pdl(perm_scan_kernel, dim3(1), dim3(1024), 0, st, E, L.nb, blk_cnt, blk_base, offsets, tiles,
                        ntiles, hdr ? hdr->counter : nullptr, hdr ? 7 : 0, tiles2, ntiles2);
     if (e == cudaSuccess)
         e = launch_pdl(perm_scatter_kernel, dim3(L.nb), dim3(L.chunk), (size_t)(L.chunk / 32) * E * sizeof(int), st,
-                       idx, A, E, blk_base, s2f, f2s, (int)none_ok, offsets);
+                       idx, A, E, blk_base, s2f, f2s, (int)none_ok, offsets, ready ? &hdr->status : nullptr);
     return e;
 }
 

@@ -204,6 +204,38 @@ def test_indices_outside_are_flagged_and_skipped(T):
 
 
 @pytest.mark.gpu
+def test_indices_outside_of_a_long_list():
+    T = 1500  # more entries than one block groups
+    x, W = rnd((T, 256), 1), weights(8, 256, 128)
+    idx, w = routing(T, 8, 4, empty=0.1)
+    bad = idx.clone()
+    bad[3, 1], bad[1207, 0], bad[T - 1, 3] = 8, -2, 2 ** 31 - 1
+    ws = api.experts_workspace(T, 256, 128, 8, 4, "cuda").fill_(0xFF)
+    for _ in range(2):
+        out = api.moe_experts(x, bad, w, *W, ws=ws)
+        assert api.moe_get_device_status(ws) == 6
+        check(out, x, torch.where((bad < 0) | (bad >= 8), -1, bad), w, *W)
+        out = api.moe_experts(x, idx, w, *W, ws=ws)
+        assert api.moe_get_device_status(ws) == api.MOE_OK
+        check(out, x, idx, w, *W)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 9, 120, 1500])
+def test_any_number_of_blocks_gives_the_same(T):
+    x, W = rnd((T, 256), 1), weights(8, 256, 192)
+    idx, w = routing(T, 8, 4, empty=0.1)
+    ref = api.moe_experts(x, idx, w, *W)
+    check(ref, x, idx, w, *W)
+    try:
+        for n in (1, 3, 40):
+            api.set_gemm_ctas(n)
+            assert torch.equal(ref, api.moe_experts(x, idx, w, *W))
+    finally:
+        api.set_gemm_ctas(0)
+
+
+@pytest.mark.gpu
 def test_streams_and_replay():
     T, H, I, E, k = 100, 256, 128, 16, 4
     x, W = rnd((T, H), 1), weights(E, H, I)

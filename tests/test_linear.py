@@ -189,6 +189,23 @@ def test_rows_and_columns_behind_aligned_outputs(M, N, K, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("M,N,ld", [(36000, 64, 60000), (36000, 70, 60001), (64, 96, 35000000)])
+def test_offsets_past_32_bits(M, N, ld):
+    # rows of out and residual more than 2^31 elements from the first
+    assert (M - 1) * ld > 2 ** 31
+    K = 72
+    x, w, _ = operands(M, N, K)
+    big = torch.empty(M * ld, dtype=torch.bfloat16, device="cuda")
+    out = big.as_strided((M, N), (ld, 1))
+    out.copy_(mat(M, N, 8))
+    check(x, w, None, "silu", out, out=out)  # onto the residual
+    ldx = ld // 8 * 8
+    far = big.as_strided((M, K), (ldx, 1))
+    far.copy_(x)
+    assert torch.equal(api.moe_linear(far, w), api.moe_linear(x.contiguous(), w))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("act", list(api.ACTS))
 @pytest.mark.parametrize("M", [5, 200, 2000])
 def test_activations_of_extreme_values(act, M):

@@ -243,6 +243,19 @@ def test_every_choice_of_many_rows(scoring, E, groups, topk_groups, k):
 
 
 @pytest.mark.gpu
+def test_offsets_past_32_bits():
+    T, E, ld = 70000, 64, 31000
+    assert (T - 1) * ld > 2 ** 31
+    x = torch.empty(T * ld, dtype=torch.bfloat16, device="cuda").as_strided((T, E), (ld, 1))
+    x.copy_(torch.randn(T, E, generator=torch.Generator(device="cuda").manual_seed(3), device="cuda"))
+    for bias in (None, a_bias(E)):
+        a, b = (api.moe_route_scored(v, 6, "sigmoid", bias) for v in (x, x.contiguous()))
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+        ri, _, _ = batch64(x.float(), 6, "sigmoid", bias, 1, 1, "max")
+        assert torch.equal(a[0], ri.int())
+
+
+@pytest.mark.gpu
 def test_given_outputs_streams_and_replay():
     x = rows(300, 256, 4, torch.float32, 11)
     b = a_bias(256)
