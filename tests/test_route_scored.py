@@ -243,6 +243,21 @@ def test_every_choice_of_many_rows(scoring, E, groups, topk_groups, k):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("E,groups,topk_groups,k", [(8, 1, 1, 8), (64, 1, 1, 6), (64, 8, 3, 6), (1000, 1, 1, 32), (256, 8, 4, 8)])
+def test_bf16_logits_of_few_values(E, groups, topk_groups, k):
+    # many equal logits, zeros of both signs, the largest finite values beside infinities
+    g = torch.Generator().manual_seed(E)
+    top = torch.finfo(torch.bfloat16).max
+    pool = torch.tensor([0.0, -0.0, 1.0, 1.0078125, -3.0, top, -top, math.inf, -math.inf, 2.0 ** -130, -2.0 ** -130, math.nan])
+    for n in (len(pool), 7, 3):
+        x = pool[torch.randint(0, n, (60, E), generator=g)].bfloat16().cuda()
+        for group_score in ("max", "top2"):
+            check(x, k, "softmax", None, groups, topk_groups, group_score)
+            check(x, k, "sigmoid", None, groups, topk_groups, group_score, True, 2.5)
+            check(x, k, "sigmoid", a_bias(E), groups, topk_groups, group_score)
+
+
+@pytest.mark.gpu
 def test_offsets_past_32_bits():
     T, E, ld = 70000, 64, 31000
     assert (T - 1) * ld > 2 ** 31
