@@ -65,7 +65,9 @@ constexpr int BN = 256;        // columns of an accumulator: two halves of up to
 //
 // A half is BH = 128 rows of B.  Batches with too few items of that width to occupy the GPU
 // take halves of 64 or 32 (moe_experts: one token, k 6 of 64 experts, H 2048, I 512: 24 gate/up
-// items of 128, 96 of 32), in more and smaller slots.
+// items of 128, 96 of 32).  Both halves then share a slot, chunk by chunk, so that one MMA of
+// N = 2 BH reads them: an MMA of M = 128 takes the 80 cycles of its A rows whatever its N, 0.7
+// us a stage of 16.
 __host__ __device__ constexpr int stages_of(int BH) { return BH == 128 ? 2 : BH == 64 ? 3 : 4; }  // A slots
 constexpr int STAGES_MAX = 4, BSLOTS_MAX = 8;
 constexpr int RING = 4;
@@ -141,13 +143,16 @@ grouped_gemm_kernel(const __grid_constant__ AMaps tmA, const __grid_constant__ C
     // Output columns per tile: the gate/up items take BH gate and the same BH up columns; the
     // down items write 2 BH columns.
     constexpr int BNO0 = BH, BNO1 = 2 * BH;
-    constexpr int STAGES = stages_of(BH), BSLOTS = 2 * STAGES, H_SUB = h_sub(BH), H_BYTES = h_bytes(BH);
+    constexpr int STAGES = stages_of(BH);
+    // B units of a stage (halves, or both in one), their rows, chunk stride and bytes
+    constexpr int UNITS = BH == 128 ? 2 : 1, BSLOTS = UNITS * STAGES, UROWS = 2 * BH / UNITS;
+    constexpr int U_SUB = h_sub(UROWS), U_BYTES = h_bytes(UROWS);
     const bool dense = g.tiles == nullptr;  // mode 2: m-tiles are plain 128-row blocks of A
     extern __shared__ uint8_t smem_raw[];
     const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
     uint8_t *sA = smem_raw + pad;
     uint8_t *sB = sA + STAGES * A_BYTES;
-    Ctrl *S = reinterpret_cast<Ctrl *>(sB + BSLOTS * H_BYTES);
+    Ctrl *S = reinterpret_cast<Ctrl *>(sB + BSLOTS * U_BYTES);
     uint8_t *turns = reinterpret_cast<uint8_t *>(S) + CTRL_BYTES;  // the epilogue warps' buffers, with g.turn_rows
 
     const int warp = uniform_warp(), lane = threadIdx.x % 32;
@@ -324,22 +329,28 @@ grouped_gemm_kernel(const __grid_constant__ AMaps tmA, const __grid_constant__ C
                 __syncwarp();
                 arm(stage, phase);
                 const int z = kb * KC;  // first K chunk of the stage
+                // gate / up rows n0.. of the expert (or of shared slice s), [KC][128], or down rows
+                // n0 + 128 half..: the expert's, or chunks of columns s*I.. of the shared down
+                auto map_of = [&](int half) { return !p1 ? half ? &tmB1 : &tmB0 : MODE == 3 ? &lm.wd : &tmB0; };
+                auto row_of = [&](int half) { return p1 ? n0 + half * BH : n0; };
 #pragma unroll 1
-                for (int half = 0; half < 2; ++half) {
+                for (int unit = 0; unit < UNITS; ++unit) {
                     if (!warp_wait(&S->bempty[bs], bphase ^ 1, g.wait_ns)) { ok = false; break; }
                     uint64_t *bar = &S->bfull[bs];
-                    uint8_t *dst = sB + bs * H_BYTES;
-                    // gate / up rows n0.. of the expert (or of shared slice s), [KC][128], or down rows
-                    // n0 + 128 half..: the expert's, or chunks of columns s*I.. of the shared down
-                    const CUtensorMap *bm = !p1 ? half ? &tmB1 : &tmB0 : MODE == 3 ? &lm.wd : &tmB0;
-                    const CUtensorMap *bsh = !p1 ? half ? &sm.b1 : &sm.b0 : MODE == 3 ? &lm.wd_sh : &sm.b0;
-                    const int brow = p1 ? n0 + half * BH : n0;
+                    uint8_t *dst = sB + bs * U_BYTES;
                     if (elect_one()) {
-                        mbar_arrive_expect_tx(bar, H_BYTES);
-                        if (tr.s < 0)
-                            tma_load_4d(dst, bm, bar, 0, brow, z, expert);
-                        else
-                            tma_load_3d(dst, bsh, bar, 0, p1 ? brow : tr.s * g.N + brow, p1 ? tr.s * (K1 / BK) + z : z);
+                        mbar_arrive_expect_tx(bar, U_BYTES);
+                        if constexpr (UNITS == 1) {  // boxes of one chunk: [KC][gate, up]
+#pragma unroll
+                            for (int b = 0; b < 2 * KC; ++b)
+                                tma_load_4d(dst + b * h_sub(BH), map_of(b & 1), bar, 0, row_of(b & 1), z + b / 2, expert);
+                        } else if (tr.s < 0) {
+                            tma_load_4d(dst, map_of(unit), bar, 0, row_of(unit), z, expert);
+                        } else {
+                            const CUtensorMap *bsh = !p1 ? unit ? &sm.b1 : &sm.b0 : MODE == 3 ? &lm.wd_sh : &sm.b0;
+                            tma_load_3d(dst, bsh, bar, 0, p1 ? row_of(unit) : tr.s * g.N + n0,
+                                        p1 ? tr.s * (K1 / BK) + z : z);
+                        }
                     }
                     __syncwarp();
                     arm(STAGES + bs, bphase);
@@ -385,7 +396,7 @@ grouped_gemm_kernel(const __grid_constant__ AMaps tmA, const __grid_constant__ C
     } else if (warp == 1) {
         // ---------------------------------------------------------- MMA issuer
         // (the whole warp, converged: warp_ptx.cuh)
-        constexpr uint32_t IDESC = idesc_bf16_f32(BM, BH);  // gate, up, or BH down columns
+        constexpr uint32_t IDESC = idesc_bf16_f32(BM, UROWS);  // gate, up, or both; or down columns
         const uint32_t sA0 = smem_u32(sA), sB0 = smem_u32(sB);
         int stage = 0, bs = 0, rs = 0, acc = 0;
         uint32_t phase = 0, bphase = 0, rphase = 0, aphase = 0;
@@ -408,21 +419,21 @@ grouped_gemm_kernel(const __grid_constant__ AMaps tmA, const __grid_constant__ C
                 const int nc = chunks_of(kb, Kd);
                 if (!warp_wait(&S->full[stage], phase, g.wait_ns)) { ok = false; break; }
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    // gate (or the first 128) columns 0..127 of the accumulator, up (or the next 128) 128..255
+                for (int unit = 0; unit < UNITS; ++unit) {
+                    // gate columns 0 .. BH - 1 of the accumulator, up the next BH; down columns all 2 BH
                     if (!warp_wait(&S->bfull[bs], bphase, g.wait_ns)) { ok = false; break; }
                     tc_fence_after();
-                    const uint32_t b0 = sB0 + bs * H_BYTES;
+                    const uint32_t b0 = sB0 + bs * U_BYTES;
                     if (elect_one()) {
 #pragma unroll
                         for (int c = 0; c < KC; ++c)
                             if (c < nc)
 #pragma unroll
                                 for (int k = 0; k < BK / 16; ++k)
-                                    mma_bf16(d + half * (BN / 2), sw128_kmajor_desc(a0 + c * A_SUB + k * 32),
-                                             sw128_kmajor_desc(b0 + c * H_SUB + k * 32), IDESC, (kb | c | k) != 0);
+                                    mma_bf16(d + unit * BH, sw128_kmajor_desc(a0 + c * A_SUB + k * 32),
+                                             sw128_kmajor_desc(b0 + c * U_SUB + k * 32), IDESC, (kb | c | k) != 0);
                         mma_commit(&S->bempty[bs]);
-                        if (half == 1) {
+                        if (unit == UNITS - 1) {
                             mma_commit(&S->empty[stage]);
                             if (kb == num_kb - 1) mma_commit(&S->accf[acc]);
                         }
@@ -479,7 +490,7 @@ grouped_gemm_kernel(const __grid_constant__ AMaps tmA, const __grid_constant__ C
                 for (int c = 0; c < BNO0 / 32; ++c) {
                     uint32_t gr[32], ur[32];
                     tmem_ld32_sync(tb + c * 32, gr);
-                    tmem_ld32_sync(tb + BN / 2 + c * 32, ur);
+                    tmem_ld32_sync(tb + BH + c * 32, ur);
                     const int col = nt * BNO0 + c * 32;
                     if (mine > 0 && col < g.N) {
                         uint32_t pk[16];
@@ -519,7 +530,7 @@ grouped_gemm_kernel(const __grid_constant__ AMaps tmA, const __grid_constant__ C
 #pragma unroll 1
                 for (int c = 0; c < BNO1 / 32; ++c) {
                     uint32_t r[32];
-                    tmem_ld32_sync(tb + (c * 32 < BH ? 0 : BN / 2 - BH) + c * 32, r);
+                    tmem_ld32_sync(tb + c * 32, r);
                     const int col = nt * BNO1 + c * 32;
                     if (mine <= 0) continue;
                     if (col < N && g.y_f32) {

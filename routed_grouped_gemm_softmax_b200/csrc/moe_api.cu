@@ -512,12 +512,13 @@ moe_status_t forward_bf16(const moe_dims_t *d, const void *x, const void *router
         const int64_t tiles = (A < d->E ? A : d->E) + A / moe::kTileRows;
         while (half > 32 && 4 * tiles * ((d->I + half - 1) / half) < 3 * moe::num_sms()) half /= 2;
     }
+    const uint32_t box_chunks = half < 128 ? 1 : 2;
     const bool direct = plan & MOE_PLAN_DIRECT_A;
     if (!moe::encode_a_maps(&tm_h, h, R, d->I, false) ||
         (!direct && !moe::encode_a_maps(&tm_xs, xs, A, d->H, false)) ||
-        !encode_4d_chunked(&tm_wg, w_gate, d->E, d->I, d->H, half, 2) ||
-        !encode_4d_chunked(&tm_wu, w_up, d->E, d->I, d->H, half, 2) ||
-        !encode_4d_chunked(&tm_wd, w_down, d->E, d->H, d->I, half, 2))
+        !encode_4d_chunked(&tm_wg, w_gate, d->E, d->I, d->H, half, box_chunks) ||
+        !encode_4d_chunked(&tm_wu, w_up, d->E, d->I, d->H, half, box_chunks) ||
+        !encode_4d_chunked(&tm_wd, w_down, d->E, d->H, d->I, half, box_chunks))
         return MOE_ERR_CUDA;
     if (direct) tm_xs = tm_h;  // no sorted copy: not loaded through
     // the shared expert: x itself as its gate/up A operand, its weights as chunked maps
