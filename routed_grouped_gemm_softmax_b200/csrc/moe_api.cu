@@ -502,15 +502,16 @@ moe_status_t forward_bf16(const moe_dims_t *d, const void *x, const void *router
     // least 768 rows per expert), on the queue's claim modes
     const int plan = bf16_plan(*d, given != nullptr);
     const bool pairs = plan & MOE_PLAN_PAIR_TILES;
-    // Rows of gate and of up an item, on a routing that is given: as many as leave items for three
-    // quarters of the SMs, were every assignment to an expert of its own (at most min(A, E)
-    // tiles, and those of full groups).  One token, k 2 of 8, H 256, I 128: 21.5 us at 128 rows, 15.3
-    // at 32; 64 tokens, k 2 of 8, I 256: 32.1 and 25.1; 512, k 2 of 8, I 1024, 128 items: 54.3
-    // at 128, 56.6 at 64.
+    // Rows of gate and of up an item, on a routing that is given: 128, but 64 where that makes fewer
+    // items than three times the SMs, and 32 where 64 make fewer than three quarters of them, were
+    // every assignment to an expert of its own (at most min(A, E) tiles, and those of full
+    // groups).  us at 128 and at 64 rows: 300 tokens k 6 of 64 experts (312 items) 58.7 and 49.2, 128
+    // k 8 of 60 75.4 and 67.1, 512 k 8 of 64 (384) 68.2 and 67.3, 2048 k 8 of 64 (768) 116.7 and 126.1;
+    // at 64 and at 32: 24 tokens k 1 of 64 (192) 31.2 and 33.7; at 128 and at 32: one, k 6, 38.2 and 26.6.
     int half = 128;
     if (given && !pairs && (plan & MOE_PLAN_LAYER_GEMM)) {
-        const int64_t tiles = (A < d->E ? A : d->E) + A / moe::kTileRows;
-        while (half > 32 && 4 * tiles * ((d->I + half - 1) / half) < 3 * moe::num_sms()) half /= 2;
+        const int64_t tiles = (A < d->E ? A : d->E) + A / moe::kTileRows, sms = moe::num_sms();
+        if (tiles * ((d->I + 127) / 128) < 3 * sms) half = 4 * tiles * ((d->I + 63) / 64) < 3 * sms ? 32 : 64;
     }
     const uint32_t box_chunks = half < 128 ? 1 : 2;
     const bool direct = plan & MOE_PLAN_DIRECT_A;
