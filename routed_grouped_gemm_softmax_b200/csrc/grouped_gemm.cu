@@ -52,8 +52,7 @@ namespace {
 
 constexpr int BM = kTileRows;  // 128 rows per tile
 constexpr int BK = 64;         // a K chunk: 64 bf16 = one 128-byte swizzle row
-constexpr int KC = 2;          // K chunks per stage
-constexpr int BKS = BK * KC;   // K of a stage: 128
+// K chunks per stage are KC: 2, or 1 (see below)
 constexpr int BN = 256;        // columns of an accumulator: two halves of up to 128
 // Stages of 128 K columns: each weight box then brings both chunks of its rows, 256
 // contiguous bytes a row, which DRAM streams about a third faster than 128-byte row
@@ -68,13 +67,15 @@ constexpr int BN = 256;        // columns of an accumulator: two halves of up to
 // items of 128, 96 of 32).  Both halves then share a slot, chunk by chunk, so that one MMA of
 // N = 2 BH reads them: an MMA of M = 128 takes the 80 cycles of its A rows whatever its N, 0.7
 // us a stage of 16.
-__host__ __device__ constexpr int stages_of(int BH) { return BH == 128 ? 2 : BH == 64 ? 3 : 4; }  // A slots
+//
+// Where the experts' rows are many the shared memory that feeds the MMAs is the bound: both halves
+// by one MMA of N = 256 read the A rows once, in stages of one chunk (KC = 1; moe_experts: 2048
+// tokens, k 6 of 64 experts 149 us and 145, 1024 k 4 of 64, I 1024, 142 and 138).
+__host__ __device__ constexpr int stages_of(int BH, int KC) { return KC == 1 ? 4 : BH == 128 ? 2 : BH == 64 ? 3 : 4; }  // A slots
 constexpr int STAGES_MAX = 4, BSLOTS_MAX = 8;
 constexpr int RING = 4;
 constexpr int A_SUB = BM * BK * 2;     // 16 KB: one chunk of A rows
-constexpr int A_BYTES = A_SUB * KC;    // 32 KB
 __host__ __device__ constexpr int h_sub(int BH) { return BH * BK * 2; }       // one chunk of half the B rows
-__host__ __device__ constexpr int h_bytes(int BH) { return h_sub(BH) * KC; }  // 32 KB of 128
 constexpr int THREADS = 192;
 constexpr uint32_t TMEM_COLS = 512;   // two 128 x 256 fp32 accumulators
 
@@ -94,9 +95,9 @@ struct Ctrl {
 };
 
 constexpr size_t CTRL_BYTES = (sizeof(Ctrl) + 127) / 128 * 128;
-constexpr size_t smem_bytes(int BH)
+constexpr size_t smem_bytes(int BH, int KC)
 {
-    return 1024 + (size_t)stages_of(BH) * (A_BYTES + 2 * h_bytes(BH)) + CTRL_BYTES;
+    return 1024 + (size_t)stages_of(BH, KC) * KC * (A_SUB + 2 * h_sub(BH)) + CTRL_BYTES;
 }
 
 __device__ __forceinline__ void record_status(int32_t *status, int code) { atomicCAS(status, 0, code); }
@@ -134,7 +135,7 @@ __device__ __forceinline__ bool wait_count_at_least(const int32_t *ctr, int targ
 
 __device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
 
-template <int MODE, int BH>
+template <int MODE, int BH, int KC>
 __global__ void __launch_bounds__(THREADS, 1)
 grouped_gemm_kernel(const __grid_constant__ AMaps tmA, const __grid_constant__ CUtensorMap tmB0,
                     const __grid_constant__ CUtensorMap tmB1, const GemmArgs g, const __grid_constant__ SharedMaps sm,
@@ -143,10 +144,10 @@ grouped_gemm_kernel(const __grid_constant__ AMaps tmA, const __grid_constant__ C
     // Output columns per tile: the gate/up items take BH gate and the same BH up columns; the
     // down items write 2 BH columns.
     constexpr int BNO0 = BH, BNO1 = 2 * BH;
-    constexpr int STAGES = stages_of(BH);
+    constexpr int STAGES = stages_of(BH, KC), BKS = BK * KC, A_BYTES = A_SUB * KC;
     // B units of a stage (halves, or both in one), their rows, chunk stride and bytes
-    constexpr int UNITS = BH == 128 ? 2 : 1, BSLOTS = UNITS * STAGES, UROWS = 2 * BH / UNITS;
-    constexpr int U_SUB = h_sub(UROWS), U_BYTES = h_bytes(UROWS);
+    constexpr int UNITS = BH == 128 && KC == 2 ? 2 : 1, BSLOTS = UNITS * STAGES, UROWS = 2 * BH / UNITS;
+    constexpr int U_SUB = h_sub(UROWS), U_BYTES = U_SUB * KC;
     const bool dense = g.tiles == nullptr;  // mode 2: m-tiles are plain 128-row blocks of A
     extern __shared__ uint8_t smem_raw[];
     const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
@@ -589,7 +590,7 @@ int num_sms()
 
 // The kernels need more than the default 48 KB of dynamic shared memory; the
 // attribute is set once per device (and per kernel) rather than on every launch.
-template <int MODE, int BH>
+template <int MODE, int BH, int KC = 2>
 static cudaError_t launch_mode(const GemmArgs &g, const AMaps &tmA, const CUtensorMap &tmB0, const CUtensorMap &tmB1,
                                const SharedMaps &s, const LayerMaps &l, cudaStream_t st)
 {
@@ -600,16 +601,16 @@ static cudaError_t launch_mode(const GemmArgs &g, const AMaps &tmA, const CUtens
     {
         std::lock_guard<std::mutex> lk(mu);
         if (!(done >> dev & 1ull)) {
-            const int a = (int)smem_bytes(BH) + 4 * kRowStoreBytes;
-            if (cudaFuncSetAttribute(grouped_gemm_kernel<MODE, BH>, cudaFuncAttributeMaxDynamicSharedMemorySize, a) !=
+            const int a = (int)smem_bytes(BH, KC) + 4 * kRowStoreBytes;
+            if (cudaFuncSetAttribute(grouped_gemm_kernel<MODE, BH, KC>, cudaFuncAttributeMaxDynamicSharedMemorySize, a) !=
                 cudaSuccess)
                 return cudaErrorInvalidValue;
             done |= 1ull << dev;
         }
     }
     const int grid = g.ctas > 0 ? g.ctas : num_sms();
-    const size_t smem = smem_bytes(BH) + (g.turn_rows ? 4 * kRowStoreBytes : 0);
-    return launch_pdl(grouped_gemm_kernel<MODE, BH>, dim3(grid), dim3(THREADS), smem, st, tmA, tmB0, tmB1, g, s, l);
+    const size_t smem = smem_bytes(BH, KC) + (g.turn_rows ? 4 * kRowStoreBytes : 0);
+    return launch_pdl(grouped_gemm_kernel<MODE, BH, KC>, dim3(grid), dim3(THREADS), smem, st, tmA, tmB0, tmB1, g, s, l);
 }
 
 cudaError_t launch_grouped_gemm(const GemmArgs &g, const AMaps &tmA, const CUtensorMap &tmB0,
@@ -628,6 +629,7 @@ cudaError_t launch_grouped_gemm(const GemmArgs &g, const AMaps &tmA, const CUten
     if (g.mode == 1) return launch_mode<1, 128>(g, tmA, tmB0, tmB1, s, l, st);
     if (g.half_rows == 32) return launch_mode<3, 32>(g, tmA, tmB0, tmB1, s, l, st);
     if (g.half_rows == 64) return launch_mode<3, 64>(g, tmA, tmB0, tmB1, s, l, st);
+    if (g.half_rows == 128) return launch_mode<3, 128, 1>(g, tmA, tmB0, tmB1, s, l, st);
     return launch_mode<3, 128>(g, tmA, tmB0, tmB1, s, l, st);
 }
 

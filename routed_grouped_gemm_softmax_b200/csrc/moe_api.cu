@@ -513,7 +513,9 @@ moe_status_t forward_bf16(const moe_dims_t *d, const void *x, const void *router
         const int64_t tiles = (A < d->E ? A : d->E) + A / moe::kTileRows, sms = moe::num_sms();
         if (tiles * ((d->I + 127) / 128) < 3 * sms) half = 4 * tiles * ((d->I + 63) / 64) < 3 * sms ? 32 : 64;
     }
-    const uint32_t box_chunks = half < 128 ? 1 : 2;
+    // and one-chunk stages for full warps of rows (grouped_gemm.cu), where DRAM is not the bound
+    const bool wide = given && !pairs && (plan & MOE_PLAN_LAYER_GEMM) && half == 128 && A / d->E >= 32;
+    const uint32_t box_chunks = half < 128 || wide ? 1 : 2;
     const bool direct = plan & MOE_PLAN_DIRECT_A;
     if (!moe::encode_a_maps(&tm_h, h, R, d->I, false) ||
         (!direct && !moe::encode_a_maps(&tm_xs, xs, A, d->H, false)) ||
@@ -569,7 +571,7 @@ moe_status_t forward_bf16(const moe_dims_t *d, const void *x, const void *router
         gl.out2 = y;
         gl.ready = at<int32_t>(ws, L.ready);
         gl.turn_rows = turn_rows;
-        gl.half_rows = half < 128 ? half : 0;
+        gl.half_rows = half < 128 || wide ? half : 0;
         gl.y_f32 = given ? at<float>(ws, L.y) : nullptr;
         if (direct) {
             gl.a_rows = s2f;

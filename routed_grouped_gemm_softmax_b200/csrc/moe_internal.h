@@ -239,7 +239,9 @@ struct GemmArgs {
     float *y_f32;
     // Full warps of h and y rows are turned in shared memory before they are stored (row_store.cuh).
     bool turn_rows;
-    int half_rows;  // mode 3: 32 or 64 rows of gate and of up an item (the maps' boxes), or 0: 128
+    // mode 3: 32, 64 or 128 rows of gate and of up an item, weight boxes of one chunk and so many rows;
+    // 0: 128 rows, boxes of two chunks
+    int half_rows;
 };
 
 // Tensor maps of the down half of the fused layer GEMM (mode 3): h as its A operand

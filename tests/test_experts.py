@@ -112,7 +112,8 @@ def test_against_64_bits(T, H, I, E, k, empty):
 # lists on both sides of what one block groups (4096 entries, 376 experts), tiles whose last rows fill part of a warp, and
 # groups of hundreds of rows
 MORE = [(512, 128, 64, 16, 8), (513, 128, 64, 16, 8), (300, 64, 64, 376, 3), (300, 64, 64, 377, 3), (400, 192, 320, 4, 4),
-        (700, 256, 64, 3, 3), (1, 2048, 512, 64, 6), (1, 64, 64, 8, 1), (4, 192, 320, 8, 2), (30, 448, 192, 16, 2), (200, 320, 1024, 2, 1), (95, 64, 64, 1, 1), (3100, 64, 192, 4, 1)]
+        (700, 256, 64, 3, 3), (1, 2048, 512, 64, 6), (1, 64, 64, 8, 1), (4, 192, 320, 8, 2), (30, 448, 192, 16, 2), (200, 320, 1024, 2, 1),
+        (1200, 64, 1024, 48, 8), (2000, 192, 640, 30, 10), (1000, 320, 1088, 31, 8), (95, 64, 64, 1, 1), (3100, 64, 192, 4, 1)]
 
 
 @pytest.mark.gpu
