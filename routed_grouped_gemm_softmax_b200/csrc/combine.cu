@@ -40,8 +40,9 @@ __device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&v)[8])
 // out[t] = bf16(sum of w[t,j] y[t*k + j] over the slots j with an expert), fp32 fma in
 // ascending j.  A slot without an expert has no y row: its memory is not read.  Bound by the
 // rows' latency where they are loaded one by one (2048 tokens, k 6, H 2048: 18.4 us, 88 MB).
-template <typename TY>
-__global__ void __launch_bounds__(256) combine_given_kernel(const TY *y, const int32_t *idx, const float *w, int H, int E,
+// PARTS: a row's second part lies `parts` rows further on.
+template <typename TY, bool PARTS>
+__global__ void __launch_bounds__(256) combine_given_kernel(const TY *y, int parts, const int32_t *idx, const float *w, int H, int E,
                                                             int k, __nv_bfloat16 *out)
 {
     constexpr int U = 4;
@@ -51,7 +52,7 @@ __global__ void __launch_bounds__(256) combine_given_kernel(const TY *y, const i
     for (int c = threadIdx.x * 8; c < H; c += 256 * 8) {
         float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         for (int j0 = 0; j0 < k; j0 += U) {  // U rows are under way at once
-            float v[U][8], g[U];
+            float v[U][8], v2[U][8], g[U];
             bool any[U];
 #pragma unroll
             for (int j = 0; j < U; ++j) {
@@ -60,12 +61,15 @@ __global__ void __launch_bounds__(256) combine_given_kernel(const TY *y, const i
             }
 #pragma unroll
             for (int j = 0; j < U; ++j)
-                if (any[j]) load8(y + (t * k + j0 + j) * H + c, v[j]);
+                if (any[j]) {
+                    load8(y + (t * k + j0 + j) * H + c, v[j]);
+                    if constexpr (PARTS) load8(y + (t * k + j0 + j + parts) * H + c, v2[j]);
+                }
 #pragma unroll
             for (int j = 0; j < U; ++j)
                 if (any[j])
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) acc[i] = fmaf(g[j], v[j][i], acc[i]);
+                    for (int i = 0; i < 8; ++i) acc[i] = fmaf(g[j], PARTS ? v[j][i] + v2[j][i] : v[j][i], acc[i]);
         }
         uint4 o;
         __nv_bfloat162 *q = reinterpret_cast<__nv_bfloat162 *>(&o);
@@ -77,13 +81,16 @@ __global__ void __launch_bounds__(256) combine_given_kernel(const TY *y, const i
 
 }  // namespace
 
-cudaError_t launch_combine_given(const void *y, bool y_f32, const int32_t *idx, const float *w, int T, int H, int E,
+cudaError_t launch_combine_given(const void *y, bool y_f32, int parts, const int32_t *idx, const float *w, int T, int H, int E,
                                  int top_k, __nv_bfloat16 *out, cudaStream_t st)
 {
-    return y_f32 ? launch_pdl(combine_given_kernel<float>, dim3(T), dim3(256), 0, st, static_cast<const float *>(y),
-                              idx, w, H, E, top_k, out)
-                 : launch_pdl(combine_given_kernel<__nv_bfloat16>, dim3(T), dim3(256), 0, st,
-                              static_cast<const __nv_bfloat16 *>(y), idx, w, H, E, top_k, out);
+    const dim3 grid(T), block(256);
+    const auto *yf = static_cast<const float *>(y);
+    if (!y_f32)
+        return launch_pdl(combine_given_kernel<__nv_bfloat16, false>, grid, block, 0, st,
+                          static_cast<const __nv_bfloat16 *>(y), 0, idx, w, H, E, top_k, out);
+    return parts ? launch_pdl(combine_given_kernel<float, true>, grid, block, 0, st, yf, parts, idx, w, H, E, top_k, out)
+                 : launch_pdl(combine_given_kernel<float, false>, grid, block, 0, st, yf, 0, idx, w, H, E, top_k, out);
 }
 
 cudaError_t launch_combine(const __nv_bfloat16 *y, const float *gate, int T, int H, int top_k,

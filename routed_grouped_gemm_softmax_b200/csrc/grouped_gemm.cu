@@ -135,7 +135,14 @@ __device__ __forceinline__ bool wait_count_at_least(const int32_t *ctr, int targ
 
 __device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
 
-template <int MODE, int BH, int KC>
+// What a value rounded to bf16 (its bits as a float's) leaves: 0 where that is infinite or NaN.
+__device__ __forceinline__ float second_part(float h, uint32_t bits)
+{
+    const float d = h - __uint_as_float(bits);
+    return fabsf(d) < INFINITY ? d : 0.0f;
+}
+
+template <int MODE, int BH, int KC, bool PARTS>
 __global__ void __launch_bounds__(THREADS, 1)
 grouped_gemm_kernel(const __grid_constant__ AMaps tmA, const __grid_constant__ CUtensorMap tmB0,
                     const __grid_constant__ CUtensorMap tmB1, const GemmArgs g, const __grid_constant__ SharedMaps sm,
@@ -304,7 +311,14 @@ grouped_gemm_kernel(const __grid_constant__ AMaps tmA, const __grid_constant__ C
             if (g4_lane && !held) load_tokens();
             // per K chunk; the weight boxes bring all KC chunks of their rows (a chunk past
             // the K range reads zeros and is not multiplied)
-            const uint32_t a_bytes = g4 ? (uint32_t)((tr.rows + 3) / 4) * 512u : (uint32_t)(a_box_rows(ab) * BK * 2);
+            const bool two = PARTS && p1;  // h rows and their second parts
+            const uint32_t a_bytes = g4 ? (uint32_t)((tr.rows + 3) / 4) * 512u
+                                        : (uint32_t)(a_box_rows(ab) * BK * 2) * (two ? 2 : 1);
+            auto load_a = [&](int s, int c, int x) {
+                uint8_t *dst = sA + s * A_BYTES + c * A_SUB;
+                tma_load_2d(dst, amap, &S->full[s], x, arow0);
+                if (two) tma_load_2d(dst + kPartRows * BK * 2, amap, &S->full[s], x, arow0 + g.parts);
+            };
             const int n0 = ip.nt * (p1 ? BNO1 : BNO0);
             const int num_kb = p1 ? kb1 : kb0;
             const int Kd = p1 ? K1 : g.K;
@@ -325,7 +339,7 @@ grouped_gemm_kernel(const __grid_constant__ AMaps tmA, const __grid_constant__ C
                     mbar_arrive_expect_tx(&S->full[stage], a_bytes * nc);
                     if (!held && !g4)
                         for (int c = 0; c < nc; ++c)
-                            tma_load_2d(sA + stage * A_BYTES + c * A_SUB, amap, &S->full[stage], (kb * KC + c) * BK, arow0);
+                            load_a(stage, c, (kb * KC + c) * BK);
                 }
                 __syncwarp();
                 arm(stage, phase);
@@ -373,7 +387,7 @@ grouped_gemm_kernel(const __grid_constant__ AMaps tmA, const __grid_constant__ C
                                 tma_gather4(sA + j * A_BYTES + c * A_SUB + lane * 512, &sm.xg, &S->full[j],
                                             (j * KC + c) * BK, tok[0], tok[1], tok[2], tok[3]);
                             else if (!g4 && lane == 0)
-                                tma_load_2d(sA + j * A_BYTES + c * A_SUB, amap, &S->full[j], (j * KC + c) * BK, arow0);
+                                load_a(j, c, (j * KC + c) * BK);
                         }
                 }
             }
@@ -481,8 +495,11 @@ grouped_gemm_kernel(const __grid_constant__ AMaps tmA, const __grid_constant__ C
                 row0 = tr.row0;
                 rows = tr.rows;
             }
-            const bool row_ok = row < rows;
-            const int mine = min(32, rows - q * 32);  // this warp's rows (0 or less: none)
+            // rows kPartRows .. of a down item's tile: the products of the second parts
+            const int second = PARTS && p1 && q * 32 >= kPartRows ? kPartRows : 0;
+            const int trow = row - second;
+            const bool row_ok = trow < rows;
+            const int mine = min(32, rows - (q * 32 - second));  // this warp's rows (0 or less: none)
             if (!mbar_wait(&S->accf[acc], aphase, g.wait_ns)) { record_status(g.status, MOE_ERR_TIMEOUT); break; }
             tc_fence_after();
             const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * BN);
@@ -501,8 +518,16 @@ grouped_gemm_kernel(const __grid_constant__ AMaps tmA, const __grid_constant__ C
                             const float h0 = silu(__uint_as_float(gr[2 * i])) * __uint_as_float(ur[2 * i]);
                             const float h1 = silu(__uint_as_float(gr[2 * i + 1])) * __uint_as_float(ur[2 * i + 1]);
                             pk[i] = pack_bf16(h0, h1);
+                            gr[2 * i] = __float_as_uint(h0), gr[2 * i + 1] = __float_as_uint(h1);
                         }
                         store_rows_bf16(turn, pk, g.out, g.N, col, row0 + row, mine, lane);
+                        if constexpr (PARTS) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                pk[i] = pack_bf16(second_part(__uint_as_float(gr[2 * i]), pk[i] << 16),
+                                                  second_part(__uint_as_float(gr[2 * i + 1]), pk[i] & 0xffff0000u));
+                            store_rows_bf16(turn, pk, g.out, g.N, col, row0 + row + g.parts, mine, lane);
+                        }
                     }
                 }
             } else if (MODE == 2) {
@@ -527,7 +552,7 @@ grouped_gemm_kernel(const __grid_constant__ AMaps tmA, const __grid_constant__ C
             } else {
                 const int N = MODE == 3 ? g.N2 : g.N;
                 __nv_bfloat16 *y = MODE == 3 ? g.out2 : g.out;
-                const int flat = row_ok ? flat_of(row0 + row) : 0;
+                const int flat = row_ok ? flat_of(row0 + trow) + (second ? g.parts : 0) : 0;
 #pragma unroll 1
                 for (int c = 0; c < BNO1 / 32; ++c) {
                     uint32_t r[32];
@@ -590,7 +615,7 @@ int num_sms()
 
 // The kernels need more than the default 48 KB of dynamic shared memory; the
 // attribute is set once per device (and per kernel) rather than on every launch.
-template <int MODE, int BH, int KC = 2>
+template <int MODE, int BH, int KC = 2, bool PARTS = false>
 static cudaError_t launch_mode(const GemmArgs &g, const AMaps &tmA, const CUtensorMap &tmB0, const CUtensorMap &tmB1,
                                const SharedMaps &s, const LayerMaps &l, cudaStream_t st)
 {
@@ -602,7 +627,7 @@ static cudaError_t launch_mode(const GemmArgs &g, const AMaps &tmA, const CUtens
         std::lock_guard<std::mutex> lk(mu);
         if (!(done >> dev & 1ull)) {
             const int a = (int)smem_bytes(BH, KC) + 4 * kRowStoreBytes;
-            if (cudaFuncSetAttribute(grouped_gemm_kernel<MODE, BH, KC>, cudaFuncAttributeMaxDynamicSharedMemorySize, a) !=
+            if (cudaFuncSetAttribute(grouped_gemm_kernel<MODE, BH, KC, PARTS>, cudaFuncAttributeMaxDynamicSharedMemorySize, a) !=
                 cudaSuccess)
                 return cudaErrorInvalidValue;
             done |= 1ull << dev;
@@ -610,7 +635,7 @@ static cudaError_t launch_mode(const GemmArgs &g, const AMaps &tmA, const CUtens
     }
     const int grid = g.ctas > 0 ? g.ctas : num_sms();
     const size_t smem = smem_bytes(BH, KC) + (g.turn_rows ? 4 * kRowStoreBytes : 0);
-    return launch_pdl(grouped_gemm_kernel<MODE, BH, KC>, dim3(grid), dim3(THREADS), smem, st, tmA, tmB0, tmB1, g, s, l);
+    return launch_pdl(grouped_gemm_kernel<MODE, BH, KC, PARTS>, dim3(grid), dim3(THREADS), smem, st, tmA, tmB0, tmB1, g, s, l);
 }
 
 cudaError_t launch_grouped_gemm(const GemmArgs &g, const AMaps &tmA, const CUtensorMap &tmB0,
@@ -627,8 +652,13 @@ cudaError_t launch_grouped_gemm(const GemmArgs &g, const AMaps &tmA, const CUten
     const LayerMaps &l = lm ? *lm : nolm;
     if (g.mode == 0) return launch_mode<0, 128>(g, tmA, tmB0, tmB1, s, l, st);
     if (g.mode == 1) return launch_mode<1, 128>(g, tmA, tmB0, tmB1, s, l, st);
-    if (g.half_rows == 32) return launch_mode<3, 32>(g, tmA, tmB0, tmB1, s, l, st);
-    if (g.half_rows == 64) return launch_mode<3, 64>(g, tmA, tmB0, tmB1, s, l, st);
+    if (g.half_rows == 32)
+        return g.parts ? launch_mode<3, 32, 2, true>(g, tmA, tmB0, tmB1, s, l, st)
+                       : launch_mode<3, 32>(g, tmA, tmB0, tmB1, s, l, st);
+    if (g.half_rows == 64)
+        return g.parts ? launch_mode<3, 64, 2, true>(g, tmA, tmB0, tmB1, s, l, st)
+                       : launch_mode<3, 64>(g, tmA, tmB0, tmB1, s, l, st);
+    if (g.parts) return launch_mode<3, 128, 2, true>(g, tmA, tmB0, tmB1, s, l, st);
     if (g.half_rows == 128) return launch_mode<3, 128, 1>(g, tmA, tmB0, tmB1, s, l, st);
     return launch_mode<3, 128>(g, tmA, tmB0, tmB1, s, l, st);
 }

@@ -513,11 +513,12 @@ moe_status_t forward_bf16(const moe_dims_t *d, const void *x, const void *router
         const int64_t tiles = (A < d->E ? A : d->E) + A / moe::kTileRows, sms = moe::num_sms();
         if (tiles * ((d->I + 127) / 128) < 3 * sms) half = 4 * tiles * ((d->I + 63) / 64) < 3 * sms ? 32 : 64;
     }
-    // and one-chunk stages for full warps of rows (grouped_gemm.cu), where DRAM is not the bound
-    const bool wide = given && !pairs && (plan & MOE_PLAN_LAYER_GEMM) && half == 128 && A / d->E >= 32;
+    const int parts = given && !pairs && (plan & MOE_PLAN_LAYER_GEMM) && A <= moe::kPartRows ? A : 0;  // h in two
+    // one-chunk stages for full warps of rows (grouped_gemm.cu), where DRAM is not the bound
+    const bool wide = given && !pairs && !parts && (plan & MOE_PLAN_LAYER_GEMM) && half == 128 && A / d->E >= 32;
     const uint32_t box_chunks = half < 128 || wide ? 1 : 2;
     const bool direct = plan & MOE_PLAN_DIRECT_A;
-    if (!moe::encode_a_maps(&tm_h, h, R, d->I, false) ||
+    if (!moe::encode_a_maps(&tm_h, h, R + parts, d->I, false) ||
         (!direct && !moe::encode_a_maps(&tm_xs, xs, A, d->H, false)) ||
         !encode_4d_chunked(&tm_wg, w_gate, d->E, d->I, d->H, half, box_chunks) ||
         !encode_4d_chunked(&tm_wu, w_up, d->E, d->I, d->H, half, box_chunks) ||
@@ -571,6 +572,7 @@ moe_status_t forward_bf16(const moe_dims_t *d, const void *x, const void *router
         gl.out2 = y;
         gl.ready = at<int32_t>(ws, L.ready);
         gl.turn_rows = turn_rows;
+        gl.parts = parts;
         gl.half_rows = half < 128 || wide ? half : 0;
         gl.y_f32 = given ? at<float>(ws, L.y) : nullptr;
         if (direct) {
@@ -625,7 +627,7 @@ moe_status_t forward_bf16(const moe_dims_t *d, const void *x, const void *router
         if (e == cudaSuccess) e = marks.mark(4, st);
     }
     if (e == cudaSuccess && given)
-        e = moe::launch_combine_given(y, true, given->idx, given->w, d->T, d->H, d->E, d->top_k,
+        e = moe::launch_combine_given(y, true, parts, given->idx, given->w, d->T, d->H, d->E, d->top_k,
                                       static_cast<__nv_bfloat16 *>(out), st);
     else if (e == cudaSuccess && !fused)
         e = moe::launch_combine(y, gate, d->T, d->H, d->top_k, static_cast<__nv_bfloat16 *>(out), st, sh, A);
@@ -711,7 +713,7 @@ moe_status_t forward_fp8(const moe_dims_t *d, const void *x, const void *router_
     }
     if (e == cudaSuccess) e = marks.mark(4, st);
     if (e == cudaSuccess && given)
-        e = moe::launch_combine_given(y, false, given->idx, given->w, d->T, d->H, d->E, d->top_k,
+        e = moe::launch_combine_given(y, false, 0, given->idx, given->w, d->T, d->H, d->E, d->top_k,
                                       static_cast<__nv_bfloat16 *>(out), st);
     else if (e == cudaSuccess && !fused)
         e = moe::launch_combine(y, gate, d->T, d->H, d->top_k, static_cast<__nv_bfloat16 *>(out), st);
@@ -791,7 +793,7 @@ moe_status_t forward_mx(const moe_dims_t *d, const void *x, const void *router_w
     if (e == cudaSuccess) e = moe::launch_grouped_gemm_mx(g2, st);
     if (e == cudaSuccess) e = marks.mark(4, st);
     if (e == cudaSuccess && given)
-        e = moe::launch_combine_given(y, false, given->idx, given->w, d->T, d->H, d->E, d->top_k,
+        e = moe::launch_combine_given(y, false, 0, given->idx, given->w, d->T, d->H, d->E, d->top_k,
                                       static_cast<__nv_bfloat16 *>(out), st);
     else if (e == cudaSuccess)
         e = moe::launch_combine(y, gate, d->T, d->H, d->top_k, static_cast<__nv_bfloat16 *>(out), st);

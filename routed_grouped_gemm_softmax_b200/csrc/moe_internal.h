@@ -13,6 +13,13 @@ namespace moe {
 
 constexpr int kTileRows = MOE_TILE_ROWS;  // BM of the grouped GEMMs
 constexpr int kMaxExperts = 1024;
+// moe_experts of at most this many assignments, by the layer GEMM, holds h as two bf16 parts, h and what its rounding
+// leaves, which lie in the two halves of the down items' 128 A rows: rows that the MMA multiplies
+// anyway.  A rounded h moves an output by about as much as the output's own rounding does (sums of many
+// rows: 1.41 of its error in all), and where rows are few a few large h can weigh more (up to 1.8).
+// One part and two, us: 1 token, k 6 of 64 experts, H 2048, I 512 27.5 and 28.7; 8, k 8 of 256 55.1 and
+// 57.9; 64, k 1 of 64, I 1024 58.1 and 59.3.
+constexpr int kPartRows = MOE_TILE_ROWS / 2;
 constexpr int kRouterKSplitMax = 8;  // K slices of the router's tensor-core logits
 
 // Header at the start of every workspace.
@@ -95,9 +102,13 @@ inline WsLayout ws_layout(const moe_dims_t &d, int dtype = MOE_DTYPE_BF16, int s
     L.xq_s = take(act_scales(static_cast<size_t>(d.T) * d.H));
     L.xs = take(A * d.H * (q8 ? 1 : 2));
     L.xs_s = take(act_scales(A * d.H));
-    L.h = take((A + SR) * d.I * (q8 ? 1 : 2));
+    // rows of h and y: twice as many in two parts, and no fewer above kPartRows than at it, so that the
+    // workspace of a batch serves smaller ones
+    const size_t PR = kPartRows;
+    const size_t HR = !given || q8 ? A : A <= PR ? 2 * A : A < 2 * PR ? 2 * PR : A;
+    L.h = take((HR + SR) * d.I * (q8 ? 1 : 2));
     L.h_s = take(act_scales(A * d.I));
-    L.y = take((A + SR) * d.H * (given && !q8 ? 4 : 2));
+    L.y = take((HR + SR) * d.H * (given && !q8 ? 4 : 2));
     L.total = o;
     return L;
 }
@@ -242,6 +253,9 @@ struct GemmArgs {
     // mode 3: 32, 64 or 128 rows of gate and of up an item, weight boxes of one chunk and so many rows;
     // 0: 128 rows, boxes of two chunks
     int half_rows;
+    // mode 3: 0, or the rows of h and of y_f32, at most kPartRows: h is held as two bf16 parts, and row r of
+    // the second at r + parts; the down items multiply both, and their y rows lie alike.
+    int parts;
 };
 
 // Tensor maps of the down half of the fused layer GEMM (mode 3): h as its A operand
@@ -383,7 +397,7 @@ cudaError_t launch_combine(const __nv_bfloat16 *y, const float *gate, int T, int
                            __nv_bfloat16 *out, cudaStream_t st, int sh_count = 0, int sh_rows0 = 0);
 // The same sum on a routing that is given: slots whose index is outside [0, E) have no y
 // row and are skipped.  y is fp32 (y_f32 true) or bf16.
-cudaError_t launch_combine_given(const void *y, bool y_f32, const int32_t *idx, const float *w, int T, int H, int E,
+cudaError_t launch_combine_given(const void *y, bool y_f32, int parts, const int32_t *idx, const float *w, int T, int H, int E,
                                  int top_k, __nv_bfloat16 *out, cudaStream_t st);
 // Scored routing of given logits (route_scored.cu): rows of E logits `ld` elements
 // apart, fp32 or (bf16 = true) bf16.

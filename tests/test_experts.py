@@ -55,7 +55,7 @@ def routing(T, E, k, seed=5, empty=0.0):
     return idx.cuda(), torch.randn(T, k, generator=g).cuda()
 
 
-def check(out, x, idx, w, w_gate, w_up, w_down):
+def check(out, x, idx, w, w_gate, w_up, w_down, eps_h=2.0 ** -8):
     H, E, I = x.shape[1], w_gate.shape[0], w_gate.shape[1]
     y = torch.zeros(x.shape, dtype=torch.float64, device="cuda")
     err = torch.zeros_like(y)
@@ -74,7 +74,7 @@ def check(out, x, idx, w, w_gate, w_up, w_down):
         ds = 1.1 * da + (8 + 2 * a.abs()) * 2.0 ** -23 * s.abs()
         h = s * u
         dh = ds * u.abs() + s.abs() * du + ds * du + 2.0 ** -24 * h.abs()
-        dh = dh + eps * (h.abs() + dh)
+        dh = dh + eps_h * (h.abs() + dh)
         D = w_down[e].double().T
         g = w[t, j].double()[:, None]
         y.index_add_(0, t, g * (h @ D))
@@ -187,6 +187,51 @@ def test_kernel_choices_agree(T):
     finally:
         for name in ("set_layer_gemm", "set_direct_a", "set_fused_combine", "set_pair_mma"):
             getattr(api, name)("auto")
+
+
+
+# up to 64 assignments h is two bf16 parts: its own rounding leaves at most 2^-8 of it, and the
+# rounding of that 2^-8 of the rest
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,H,I,E,k", [(1, 256, 128, 8, 8), (64, 128, 64, 3, 1), (16, 320, 192, 8, 4), (8, 64, 1088, 60, 8),
+                                       (63, 192, 2048, 1, 1), (32, 2048, 64, 16, 2), (2, 64, 4096, 64, 32)])
+@pytest.mark.parametrize("one", [False, True])
+def test_h_of_few_rows_in_two_parts(T, H, I, E, k, one):
+    x, W = rnd((T, H), 1), weights(E, H, I)
+    idx, w = routing(T, E, k, empty=0.1)
+    if one:  # a tile of all the rows
+        idx.fill_(E - 1)
+    ws = api.experts_workspace(T, H, I, E, k, "cuda").fill_(0xFF)
+    try:
+        for layer in ("auto", "always"):
+            for direct in ("auto", "always", "never"):
+                api.set_layer_gemm(layer)
+                api.set_direct_a(direct)
+                out = api.moe_experts(x, idx, w, *W, ws=ws)
+                assert api.moe_get_device_status(ws) == api.MOE_OK
+                check(out, x, idx, w, *W, eps_h=2.0 ** -16)
+    finally:
+        api.set_layer_gemm("auto")
+        api.set_direct_a("auto")
+
+
+@pytest.mark.parametrize("H,I,E,k", [(256, 128, 8, 1), (128, 4096, 300, 1), (2048, 512, 64, 3)])
+def test_a_batch_s_workspace_serves_smaller_ones(H, I, E, k):
+    build.build()
+    sizes = [api.lib().moe_experts_workspace_size(ctypes.byref(api.dims(T, H, I, E, k)), 0) for T in range(1, 300)]
+    assert sizes == sorted(sizes) and sizes[0] > 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [2, 65])
+def test_infinite_h_stays_infinite(T):
+    H = I = 64
+    x = torch.full((T, H), 1e20, dtype=torch.bfloat16, device="cuda")
+    x[1] = float("nan")
+    ones = torch.ones(1, 64, 64, dtype=torch.bfloat16, device="cuda")
+    idx, w = torch.zeros(T, 1, dtype=torch.int32, device="cuda"), torch.ones(T, 1, device="cuda")
+    out = api.moe_experts(x, idx, w, ones, ones, ones)
+    assert bool(out[1].isnan().all()) and bool((out[0] == float("inf")).all()) and bool((out[2:] == float("inf")).all())
 
 
 @pytest.mark.gpu
