@@ -235,9 +235,9 @@ grouped_gemm_kernel(const __grid_constant__ AMaps tmA, const __grid_constant__ C
 
     if (warp == 0) {
         // ------------------------------------------------ scheduler + TMA producer
-        // Lane 0 claims the items, keeps the rings and loads B (and A with row-block
-        // boxes); with direct A rows (GemmArgs::a_rows) each lane gathers four A rows of a
-        // routed gate/up tile per stage, lane l rows 4l..4l+3.
+        // Lane 0 claims the items and keeps the rings; an elected lane loads B (and A with
+        // row-block boxes); with direct A rows (GemmArgs::a_rows) each lane gathers four A rows
+        // of a routed gate/up tile per stage, lane l rows 4l..4l+3.
         const bool gather = (MODE == 0 || MODE == 3) && g.a_rows != nullptr;
         const int total = MODE == 3 ? total0 + mtiles * nt1 : mtiles * (MODE == 0 ? nt0 : nt1);
         int stage = 0, bs = 0, rs = 0;
@@ -325,11 +325,12 @@ grouped_gemm_kernel(const __grid_constant__ AMaps tmA, const __grid_constant__ C
             if (MODE == 3 && p1) {
                 // the down item reads h rows of m-tile mt: wait until every gate/up item of
                 // mt has published them, then order those generic-proxy writes before the
-                // TMA (async-proxy) reads below
-                if (lane == 0) {
-                    okl = wait_count_at_least(g.ready + ip.mt, 4 * nt0, g.wait_ns);
-                    fence_proxy_async_global();
-                }
+                // TMA (async-proxy) reads below.  A proxy fence holds for the lane that runs it and
+                // the loads are an elected lane's, so every lane is behind lane 0's acquire
+                // (the barrier; a shuffle orders no memory) and fences.
+                if (lane == 0) okl = wait_count_at_least(g.ready + ip.mt, 4 * nt0, g.wait_ns);
+                __syncwarp();
+                fence_proxy_async_global();
                 if (!__shfl_sync(0xffffffffu, okl, 0)) { ok = false; break; }
             }
             for (int kb = 0; kb < num_kb; ++kb) {
@@ -381,14 +382,17 @@ grouped_gemm_kernel(const __grid_constant__ AMaps tmA, const __grid_constant__ C
                     pdl_wait();
                     held = false;
                     if (g4_lane) load_tokens();
+                    __syncwarp();
+                    const bool issues = elect_one();  // the lane of the other row-block loads
                     for (int j = 0; j <= kb; ++j)
                         for (int c = 0; c < chunks_of(j, Kd); ++c) {
                             if (g4_lane)
                                 tma_gather4(sA + j * A_BYTES + c * A_SUB + lane * 512, &sm.xg, &S->full[j],
                                             (j * KC + c) * BK, tok[0], tok[1], tok[2], tok[3]);
-                            else if (!g4 && lane == 0)
+                            else if (!g4 && issues)
                                 load_a(j, c, (j * KC + c) * BK);
                         }
+                    __syncwarp();
                 }
             }
             if (!ok) break;

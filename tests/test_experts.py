@@ -395,3 +395,31 @@ def test_a_layer_of_scored_router_experts_and_shared_dense(T):
     assert api.moe_get_device_status(ews) == api.MOE_OK and api.moe_get_device_status(lws) == api.MOE_OK
     for a, b in zip(layer(), got):
         assert torch.equal(a, b)
+
+
+# each form of the experts' GEMM: rows of gate and of up an item, K chunks a stage, parts of h
+FORMS = {"32 rows, h in two parts": (1, 2048, 512, 64, 6), "64 rows, two parts": (8, 256, 512, 64, 8),
+         "128 rows, two parts": (16, 256, 1024, 64, 4), "32 rows": (9, 256, 128, 8, 8), "64 rows": (40, 256, 512, 64, 8),
+         "128 rows, rows gathered from x": (80, 256, 1024, 64, 8), "128 rows, two chunks": (160, 256, 1024, 64, 8),
+         "128 rows, one chunk": (1024, 256, 1024, 64, 4), "pairs": (1600, 256, 128, 2, 1)}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("form", list(FORMS))
+def test_down_items_read_the_h_of_their_own_call(form):
+    """Calls of different inputs on one workspace, nothing between them: a down item that read h
+    before it saw the other blocks' stores would find the rows of the call before."""
+    T, H, I, E, k = FORMS[form]
+    W = weights(E, H, I)
+    idx, w = routing(T, E, k, empty=0.1)
+    xs = [rnd((T, H), 60 + i) for i in range(3)]
+    want = []
+    for x in xs:
+        want.append(api.moe_experts(x, idx, w, *W))
+        torch.cuda.synchronize()
+        check(want[-1], x, idx, w, *W)
+    ws = api.experts_workspace(T, H, I, E, k, "cuda")
+    outs = [api.moe_experts(xs[i % 3], idx, w, *W, ws=ws) for i in range(60)]
+    assert api.moe_get_device_status(ws) == api.MOE_OK
+    for i, out in enumerate(outs):
+        assert torch.equal(out, want[i % 3]), i
