@@ -233,7 +233,8 @@ moe_status_t moe_forward_shared(const moe_dims_t *d, const void *x, const void *
  * MOE_ERR_INVALID_ARG: N or K <= 0, a row stride below the row's length, ldx or ldw not a
  * multiple of 8 (the stride of a single row is not read), x, w or w_up not 16-byte
  * aligned, bias_up without w_up, an unknown enum value, other pointers not aligned to
- * their elements.  M == 0 is a no-op that returns MOE_OK. */
+ * their elements.  MOE_ERR_UNSUPPORTED: M, N or K above 2^31 - 256, strides of 2^38 or more, more
+ * output tiles than a grid holds.  M == 0 is a no-op that returns MOE_OK. */
 enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_GELU = 2, MOE_ACT_GELU_TANH = 3, MOE_ACT_SILU = 4 };
 enum { MOE_OUT_BF16 = 0, MOE_OUT_F32 = 1 };
 typedef struct {

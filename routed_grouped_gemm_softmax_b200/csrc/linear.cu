@@ -473,6 +473,9 @@ moe_status_t moe_linear(const moe_linear_t *d, const void *x, const void *w, con
         return MOE_ERR_INVALID_ARG;
     if (d->N > 1 && (d->ldw < d->K || d->ldw % 8)) return MOE_ERR_INVALID_ARG;
     if (bias_up && !w_up) return MOE_ERR_INVALID_ARG;
+    // sizes are rounded up to whole tiles (of up to 256 rows, 128 of K) in 32 bits
+    const int32_t most = INT32_MAX - 255;
+    if (d->M > most || d->N > most || d->K > most) return MOE_ERR_UNSUPPORTED;
     const int64_t far = (int64_t)1 << 38;  // a tensor map's stride is below 2^40 bytes
     if (d->ldx >= far || d->ldw >= far) return MOE_ERR_UNSUPPORTED;
     if (((int64_t)d->M + 15) / 16 * (((int64_t)d->N + 127) / 128) > INT32_MAX / 8) return MOE_ERR_UNSUPPORTED;

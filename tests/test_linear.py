@@ -40,6 +40,20 @@ def test_host_refusals():
     assert call(lin(M=0), None, None, None, None, None, None, None, None, 0) == 0
 
 
+def test_sizes_that_no_longer_round_up_in_32_bits_are_refused():
+    build.build()
+    L = api.lib()
+    buf = ctypes.create_string_buffer(8192)
+    p = (ctypes.addressof(buf) + 255) // 256 * 256
+    most = 2 ** 31 - 256
+    for over in (most + 1, 2 ** 31 - 1):
+        for d in (lin(M=over, N=8, K=8), lin(M=1, N=over, K=8), lin(M=1, N=1, K=over, ldx=8, ldw=8)):
+            # without a workspace: what is let through comes to that check and no further
+            assert L.moe_linear(ctypes.byref(d), p, p, None, None, None, None, p, None, 0, None) == 2
+    for d in (lin(M=most, N=8, K=8), lin(M=1, N=most, K=8), lin(M=1, N=1, K=most, ldx=8, ldw=8)):
+        assert L.moe_linear(ctypes.byref(d), p, p, None, None, None, None, p, None, 0, None) == 3
+
+
 def test_python_refusals_need_no_gpu():
     with pytest.raises(ValueError):
         api.moe_linear(torch.zeros(4, 8).bfloat16(), torch.zeros(4, 8).bfloat16())
