@@ -207,7 +207,14 @@ def _call(fn, where, dev, stream, *args):
         raise MoEError(code, where)
 
 
+def _need_i32(where, *sizes):
+    """Refuses numbers that a 32-bit field of the C structures would wrap without a word."""
+    if max(sizes) > 0x7FFFFFFF or min(sizes) < -0x80000000:
+        raise MoEError(2, where)
+
+
 def dims(T, H, I, E, top_k) -> Dims:
+    _need_i32("sizes", T, H, I, E, top_k)
     return Dims(int(T), int(H), int(I), int(E), int(top_k))
 
 
@@ -259,6 +266,7 @@ def moe_route_scored(logits, top_k: int, scoring: str = "softmax", bias=None, n_
         raise ValueError(f"logits: expected a CUDA matrix [T, E], got {tuple(logits.shape)} on {logits.device}")
     T, E = logits.shape
     dev = logits.device
+    _need_i32("moe_route_scored", T, E, top_k, n_groups, topk_groups)
     ld = _rows_of(logits, dev, (torch.float32, torch.bfloat16), logits.shape, "logits")
     if bias is not None:
         _need_on(bias, dev, torch.float32, (E,), "bias")
@@ -457,6 +465,7 @@ def moe_linear(x, w, bias=None, act: str = "none", residual=None, w_up=None, bia
     M, K = x.shape
     N = w.shape[0]
     dev = x.device
+    _need_i32("moe_linear", M, N, K)
     ldx = _rows_of(x, dev, _BF16, (M, K), "x")
     ldw = _rows_of(w, dev, _BF16, (N, K), "w")
     if w_up is not None and _rows_of(w_up, dev, _BF16, (N, K), "w_up") != ldw:

@@ -39,6 +39,17 @@ def test_host_refusals():
         assert fn(*([b(api.dims(0, 512, 512, 8, 2))] + [None] * (len(good) - 3) + [0, None])) == 0
 
 
+def test_sizes_past_32_bits_are_refused():
+    build.build()
+    for at in range(5):
+        sizes = [4, 512, 512, 8, 2]
+        sizes[at] += 1 << 32  # 4 tokens, 8 experts and so on, were they wrapped
+        for call in (lambda: api.dims(*sizes), lambda: api.experts_workspace(*sizes, device="cpu")):
+            with pytest.raises(api.MoEError) as e:
+                call()
+            assert e.value.code == 2
+
+
 def rnd(shape, seed, std=1.0, dtype=torch.bfloat16):
     g = torch.Generator(device="cuda").manual_seed(seed)
     return (torch.randn(*shape, generator=g, device="cuda") * std).to(dtype)

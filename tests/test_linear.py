@@ -334,3 +334,13 @@ def test_python_refusals():
         with pytest.raises(api.MoEError):
             bad()
     assert api.moe_linear(x[:0], w).shape == (0, 16)
+
+
+@pytest.mark.gpu
+def test_sizes_past_32_bits_are_refused():
+    # 2^32 + 4 rows are not 4
+    big = torch.empty(1, 8, dtype=torch.bfloat16, device="cuda").expand(2 ** 32 + 4, 8)
+    for bad in (lambda: api.moe_linear(big, big[:1]), lambda: api.moe_linear(big[:1], big)):
+        with pytest.raises(api.MoEError) as e:
+            bad()
+        assert e.value.code == 2

@@ -313,3 +313,14 @@ def test_python_refusals():
             bad()
     i, w = api.moe_route_scored(x[:0], 2)
     assert i.shape == (0, 2) and w.shape == (0, 2)
+
+
+@pytest.mark.gpu
+def test_sizes_past_32_bits_are_refused():
+    # 2^32 + 4 rows are not 4
+    x, big = rows(4, 16), torch.empty(2 ** 32 + 4, 1, dtype=torch.bfloat16, device="cuda")
+    for bad in (lambda: api.moe_route_scored(big, 1), lambda: api.moe_route_scored(x, 2, n_groups=2 ** 32 + 1),
+                lambda: api.moe_route_scored(x, 2, n_groups=4, topk_groups=2 ** 32 + 2)):
+        with pytest.raises(api.MoEError) as e:
+            bad()
+        assert e.value.code == 2
