@@ -172,6 +172,12 @@ def _need_on(t, dev, dtype, shape, name):
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
+def _need_ws(ws, dev):
+    """A workspace is as many bytes as it has elements: one that repeats or skips memory would be written past its end."""
+    if ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"ws: expected contiguous memory on {dev}, got strides {ws.stride()} on {ws.device}")
+
+
 def _rows_of(t, dev, dtypes, shape, name) -> int:
     """The row stride, in elements, of a matrix of this shape whose rows are contiguous."""
     if t.dtype in dtypes and t.shape == shape and t.device == dev:
@@ -357,8 +363,8 @@ def _experts(fn, where, dtype, x, topk_idx, topk_w, E, I, weights, out, ws, stre
         _need_on(out, dev, torch.bfloat16, (T, H), "out")
     if ws is None:
         ws = experts_workspace(T, H, I, E, k, dev, dtype, stream)
-    elif ws.device != dev:
-        raise ValueError(f"ws: on {ws.device}, expected {dev}")
+    else:
+        _need_ws(ws, dev)
     d = dims(T, H, I, E, k)
     _call(fn, where, dev, stream, ctypes.byref(d), x.data_ptr(), topk_idx.data_ptr(), topk_w.data_ptr(),
           *[t.data_ptr() for t, _, _, _ in weights], out.data_ptr(), ws.data_ptr(), ws.numel())
@@ -483,8 +489,8 @@ def moe_linear(x, w, bias=None, act: str = "none", residual=None, w_up=None, bia
         ldo = _rows_of(out, dev, (out_dtype,), (M, N), "out")
     if ws is None:
         ws = linear_workspace(dev, stream)
-    elif ws.device != dev:
-        raise ValueError(f"ws: on {ws.device}, expected {dev}")
+    else:
+        _need_ws(ws, dev)
     d = Linear(M, N, K, ACTS[act], out_dtype == torch.float32, ldx, ldw, ldr, ldo)
     _call(lib().moe_linear, "moe_linear", dev, stream, ctypes.byref(d), x.data_ptr(), w.data_ptr(),
           None if w_up is None else w_up.data_ptr(), None if bias is None else bias.data_ptr(),

@@ -50,6 +50,17 @@ def test_sizes_past_32_bits_are_refused():
             assert e.value.code == 2
 
 
+def test_a_workspace_is_contiguous_memory_of_the_device():
+    cpu = torch.device("cpu")
+    api._need_ws(torch.zeros(64, dtype=torch.uint8), cpu)
+    for ws in (torch.zeros(1, dtype=torch.uint8).expand(64), torch.zeros(8, dtype=torch.uint8).expand(8, 8),
+               torch.zeros(128, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError):
+            api._need_ws(ws, cpu)
+    with pytest.raises(ValueError):
+        api._need_ws(torch.zeros(64, dtype=torch.uint8, device="meta"), cpu)
+
+
 def rnd(shape, seed, std=1.0, dtype=torch.bfloat16):
     g = torch.Generator(device="cuda").manual_seed(seed)
     return (torch.randn(*shape, generator=g, device="cuda") * std).to(dtype)
@@ -434,3 +445,16 @@ def test_down_items_read_the_h_of_their_own_call(form):
     assert api.moe_get_device_status(ws) == api.MOE_OK
     for i, out in enumerate(outs):
         assert torch.equal(out, want[i % 3]), i
+
+
+@pytest.mark.gpu
+def test_workspaces_that_repeat_memory_are_refused():
+    from test_linear import operands
+    x, W = rnd((4, 64), 1), weights(4, 64, 64)
+    idx, w = routing(4, 4, 2)
+    ws = torch.zeros(1, dtype=torch.uint8, device="cuda").expand(1 << 24)
+    y, v, _ = operands(4, 16, 32)
+    for bad in (lambda: api.moe_experts(x, idx, w, *W, ws=ws), lambda: api.moe_experts(x, idx, w, *W, ws=ws[:1].cpu()),
+                lambda: api.moe_linear(y, v, ws=ws), lambda: api.moe_linear(y, v, ws=ws[:1].cpu())):
+        with pytest.raises(ValueError):
+            bad()
