@@ -474,7 +474,7 @@ def moe_linear(x, w, bias=None, act: str = "none", residual=None, w_up=None, bia
     _need_i32("moe_linear", M, N, K)
     ldx = _rows_of(x, dev, _BF16, (M, K), "x")
     ldw = _rows_of(w, dev, _BF16, (N, K), "w")
-    if w_up is not None and _rows_of(w_up, dev, _BF16, (N, K), "w_up") != ldw:
+    if w_up is not None and _rows_of(w_up, dev, _BF16, (N, K), "w_up") != ldw and N > 1:
         raise ValueError("w_up: its rows must be as far apart as those of w")
     if bias is not None:
         _need_on(bias, dev, torch.float32, (N,), "bias")

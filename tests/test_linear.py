@@ -344,3 +344,12 @@ def test_sizes_past_32_bits_are_refused():
         with pytest.raises(api.MoEError) as e:
             bad()
         assert e.value.code == 2
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [1, 5, 300])
+def test_one_column_whose_gate_and_up_rows_lie_apart(M):
+    # of a single row no stride is read: w a row of a wide matrix, w_up one of its own
+    x, w, u = mat(M, 64, 1), mat(1, 64, 2, 24), mat(1, 64, 3)
+    check(x, w, None, "silu", None, u)
+    check(x, u, None, "silu", None, w)
