@@ -458,3 +458,25 @@ def test_workspaces_that_repeat_memory_are_refused():
                 lambda: api.moe_linear(y, v, ws=ws), lambda: api.moe_linear(y, v, ws=ws[:1].cpu())):
         with pytest.raises(ValueError):
             bad()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("form", [f for f in FORMS if f != "pairs"])  # their MMA warp has no stall hook
+def test_a_wait_that_runs_out_is_reported_and_recoverable(form):
+    # the MMA warps wait 20 ms for what never comes: every role unwinds behind its own copies, and the
+    # next call on the same workspace has the result of an undisturbed one
+    T, H, I, E, k = FORMS[form]
+    x, W = rnd((T, H), 1), weights(E, H, I)
+    idx, w = routing(T, E, k, empty=0.1)
+    ws = api.experts_workspace(T, H, I, E, k, "cuda")
+    ref = api.moe_experts(x, idx, w, *W, ws=ws)
+    assert api.moe_get_device_status(ws) == api.MOE_OK
+    check(ref, x, idx, w, *W)
+    api.set_wait_limit_us(20000, stall_test=True)
+    try:
+        api.moe_experts(x, idx, w, *W, ws=ws)
+        assert api.moe_get_device_status(ws) == 5
+    finally:
+        api.set_wait_limit_us(0)
+    assert torch.equal(ref, api.moe_experts(x, idx, w, *W, ws=ws))
+    assert api.moe_get_device_status(ws) == api.MOE_OK
