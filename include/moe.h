@@ -124,8 +124,11 @@ moe_status_t moe_route(const moe_dims_t *d, const void *x, const void *router_w,
  * An expert is available to a row unless its logit or its bias is NaN or -inf; a +inf
  * logit counts as the largest finite float.  Slots for which no available expert is
  * left hold index -1 and weight 0 (all of them in a padded row of -inf): moe_experts
- * skips them.  Choices are those of 64-bit scores, whatever the order of evaluation;
- * weights are fp32.
+ * skips them.  Choices are those of p, p + bias and a group's sum of two each taken in 64
+ * bits, never of fp32 scores.  What only the roundings of those 64 bits tell apart may go
+ * either way: values that are equal in exact arithmetic but summed of other terms (two
+ * groups of the same p's whose biases have one sum), or closer than about 2^-50 of them.
+ * Equal logits with equal biases tie exactly.  Weights are fp32, within a few steps of it.
  *   logits [T, E] fp32 or bf16, rows `ld` >= E elements apart; bias [E] fp32, nullable
  *   ->  topk_idx [T, top_k] int32, topk_w [T, top_k] fp32
  * MOE_ERR_INVALID_ARG: as the rules above, E not a multiple of n_groups, topk_groups

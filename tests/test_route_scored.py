@@ -1,6 +1,7 @@
 """moe_route_scored: refusals on the host, and the GPU kernel against a 64-bit NumPy form of the
 same definition (choices equal, weights within the rounding of their fp32 evaluation)."""
 import ctypes
+import itertools
 import math
 
 import numpy as np
@@ -324,3 +325,40 @@ def test_sizes_past_32_bits_are_refused():
         with pytest.raises(api.MoEError) as e:
             bad()
         assert e.value.code == 2
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,topk_groups,k", [(64, 8, 3, 8), (120, 4, 2, 16), (160, 8, 3, 6), (256, 8, 4, 8), (512, 16, 4, 8),
+                                                    (1024, 32, 4, 30)])
+def test_rows_whose_groups_tie_but_for_64_bit_roundings(scoring, E, groups, topk_groups, k):
+    """The rows that batch64 leaves open: the choice is that of some set of groups that takes every
+    group clearly above the cut and fills up with those at it, and exact within that set."""
+    T, n = 20000, E // groups
+    g = torch.Generator().manual_seed(E + k)
+    bias = ((torch.randn(E, generator=g) * 4).round() / 64).cuda()
+    seen = 0
+    for logits in ((torch.randn(T, E, generator=g) * 2).round() / 2, torch.randint(0, 2, (T, E), generator=g).float()):
+        x = logits.cuda()
+        idx, w = api.moe_route_scored(x, k, scoring, bias, groups, topk_groups, "top2", False)
+        _, _, open_ = batch64(x, k, scoring, bias, groups, topk_groups, "top2")
+        rows_ = open_.nonzero()[:300, 0]
+        seen += rows_.numel()
+        z = x[rows_].double()
+        p = torch.sigmoid(z) if scoring == "sigmoid" else torch.softmax(z, 1)
+        c = p + bias.double()
+        v = c.view(-1, groups, n).sort(dim=2, descending=True).values[:, :, :2].sum(2)
+        for p_, c_, v_, i_, w_ in zip(*(t.cpu().numpy() for t in (p, c, v, idx[rows_], w[rows_].double()))):
+            cut = np.sort(v_)[-topk_groups]
+            above = [h for h in range(groups) if v_[h] > cut + 2.0 ** -49]
+            at = [h for h in range(groups) if abs(v_[h] - cut) <= 2.0 ** -49]
+            assert len(above) < topk_groups <= len(above) + len(at)
+            found = False
+            for more in itertools.combinations(at, topk_groups - len(above)):
+                kept = np.isin(np.arange(E) // n, above + list(more))
+                want = np.argsort(-np.where(kept, c_, -np.inf), kind="stable")[:k]
+                found = found or np.array_equal(want, i_)
+            assert found, (i_, v_)
+            # as in the test of every choice
+            assert np.all(np.abs(w_ - p_[i_]) <= 2.0 ** -24 * (60 + 4 + 60 + 4 + 37 + 4) * p_[i_])
+    assert seen > 0
