@@ -183,7 +183,10 @@ moe_status_t moe_forward(const moe_dims_t *d, const void *x, const void *router_
  * and flagged MOE_ERR_BAD_INDEX.  An expert may come twice in a token.  The kernels and
  * roundings are moe_forward's (moe_forward_fp8's, moe_forward_mx's) but for the bf16
  * form's per-assignment expert outputs, which stay in fp32 until the weighted sum, and
- * its h of up to 64 assignments (T*k), which keeps 16 bits and more (two bf16 parts).
+ * its h of up to 64 assignments (T*k), which keeps 16 bits and more (two bf16 parts) unless
+ * moe_set_layer_gemm(2) or moe_set_pair_mma(1) chooses kernels that round it once, as it
+ * is for more assignments.  So a token's bits depend on its company in one way: whether
+ * its batch has more than 64 assignments.
  * ws_bytes >= moe_experts_workspace_size(d, dtype), the dtype that of the weights; other
  * rules as the forward of that dtype. */
 size_t moe_experts_workspace_size(const moe_dims_t *d, int dtype);

@@ -380,7 +380,8 @@ def _experts_shape(x, w_gate):
 
 def moe_experts(x, topk_idx, topk_w, w_gate, w_up, w_down, out=None, ws=None, stream=None):
     """The experts' products on a given routing: topk_idx int32 [T,k] (-1: no expert), topk_w
-    fp32 [T,k]; weights as moe_forward's; ws from experts_workspace; returns out bf16 [T,H]."""
+    fp32 [T,k]; weights as moe_forward's; ws from experts_workspace; returns out bf16 [T,H].
+    The hidden rows are rounded to bf16 once from 65 assignments (T*k) on and keep 16 bits and more below."""
     H, E, I = _experts_shape(x, w_gate)
     b = torch.bfloat16
     return _experts(lib().moe_experts, "moe_experts", DTYPE_BF16, x, topk_idx, topk_w, E, I,

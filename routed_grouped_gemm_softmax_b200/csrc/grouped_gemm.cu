@@ -524,8 +524,10 @@ grouped_gemm_kernel(const __grid_constant__ AMaps tmA, const __grid_constant__ C
                             pk[i] = pack_bf16(h0, h1);
                             gr[2 * i] = __float_as_uint(h0), gr[2 * i + 1] = __float_as_uint(h1);
                         }
+                        // h is rounded to the down MMAs' operand type, once (over many rows 1.41 times the error
+                        // of a rounded output in all; a second MMA for the rest would double the down items' work)
                         store_rows_bf16(turn, pk, g.out, g.N, col, row0 + row, mine, lane);
-                        if constexpr (PARTS) {
+                        if constexpr (PARTS) {  // few rows: kept in two parts (kPartRows)
 #pragma unroll
                             for (int i = 0; i < 16; ++i)
                                 pk[i] = pack_bf16(second_part(__uint_as_float(gr[2 * i]), pk[i] << 16),

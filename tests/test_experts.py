@@ -480,3 +480,40 @@ def test_a_wait_that_runs_out_is_reported_and_recoverable(form):
         api.set_wait_limit_us(0)
     assert torch.equal(ref, api.moe_experts(x, idx, w, *W, ws=ws))
     assert api.moe_get_device_status(ws) == api.MOE_OK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,H,I,E,k", [(1, 256, 128, 8, 8), (16, 320, 192, 8, 4), (8, 64, 1088, 60, 8), (64, 128, 64, 3, 1)])
+def test_few_rows_by_the_other_kernels_round_h_once(T, H, I, E, k):
+    x, W = rnd((T, H), 1), weights(E, H, I)
+    idx, w = routing(T, E, k, empty=0.1)
+    ws = api.experts_workspace(T, H, I, E, k, "cuda").fill_(0xFF)
+    for name, mode in (("set_layer_gemm", "never"), ("set_pair_mma", "always")):
+        for direct in ("always", "never"):
+            try:
+                getattr(api, name)(mode)
+                api.set_direct_a(direct)
+                out = api.moe_experts(x, idx, w, *W, ws=ws)
+                assert api.moe_get_device_status(ws) == api.MOE_OK
+                check(out, x, idx, w, *W)  # eps_h: one rounding
+            finally:
+                getattr(api, name)("auto")
+                api.set_direct_a("auto")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H,I,E,k", [(320, 192, 16, 8), (512, 1024, 64, 8)])
+def test_a_token_s_bits_depend_on_its_company_only_through_h(H, I, E, k):
+    # batches of up to 64 assignments agree among themselves and larger ones do, whatever kernels their sizes choose
+    n = 900 * E // k  # pair tiles at the end
+    x, W = rnd((n, H), 1), weights(E, H, I)
+    g = torch.Generator().manual_seed(5)
+    idx = torch.rand(n, E, generator=g).argsort(1)[:, :k].int().cuda()
+    w = torch.randn(n, k, generator=g).cuda()
+    few = 64 // k
+    small = api.moe_experts(x[:few], idx[:few], w[:few], *W)
+    for T in range(1, few):
+        assert torch.equal(api.moe_experts(x[:T], idx[:T], w[:T], *W), small[:T]), T
+    large = api.moe_experts(x, idx, w, *W)
+    for T in (few + 1, 2 * few, 5 * few, 20 * few, 100 * few, n // 10, n // 3):
+        assert torch.equal(api.moe_experts(x[:T], idx[:T], w[:T], *W), large[:T]), T
