@@ -65,8 +65,9 @@ constexpr int BN = 256;        // columns of an accumulator: two halves of up to
 // A half is BH = 128 rows of B.  Batches with too few items of that width to occupy the GPU
 // take halves of 64 or 32 (moe_experts: one token, k 6 of 64 experts, H 2048, I 512: 24 gate/up
 // items of 128, 96 of 32).  Both halves then share a slot, chunk by chunk, so that one MMA of
-// N = 2 BH reads them: an MMA of M = 128 takes the 80 cycles of its A rows whatever its N, 0.7
-// us a stage of 16.
+// N = 2 BH reads them.  An MMA of M = 128 and K = 16 takes 49 cycles at N = 16 to 64, 64 at N = 128
+// and 128 at N = 256 (issued back to back by a converged warp): one for both halves of 64 rows 64
+// cycles, two 98; of 32 rows 49 and 97.
 //
 // Where the experts' rows are many the shared memory that feeds the MMAs is the bound: both halves
 // by one MMA of N = 256 read the A rows once, in stages of one chunk (KC = 1; moe_experts: 2048

@@ -33,7 +33,7 @@
 namespace moe {
 namespace {
 
-constexpr int kWarps = 4;  // tokens per CTA
+constexpr int kWarps = 4;  // warps per CTA: a token each, or 32 / G where one has G lanes
 constexpr unsigned kFull = 0xffffffffu;
 
 __device__ __forceinline__ float load_logit(const float *p) { return *p; }

@@ -4,8 +4,10 @@
 // Those instructions take addresses, descriptors and coordinates from uniform registers.
 // In a branch that lane 0 takes by its index nothing can be computed there, and each operand
 // of each instruction is moved over on its own: issuing one 128 x N x 16 MMA took 80
-// cycles (the tensor core needs 64 at N = 128).  A warp that stays converged, its index
-// read by a shuffle, computes them in place, and elect.sync marks a branch as one lane's.
+// cycles in the dense products' loop.  A warp that stays converged, its index read by a shuffle,
+// computes them in place (32 cycles there), and elect.sync marks a branch as one lane's.
+// Back to back, without a loop's waits, an MMA of N <= 64 takes 64 cycles from lane 0 and 49 so;
+// from N = 128 on, 64 cycles (128 at N = 256), the tensor core is the bound either way.
 #pragma once
 #include "sm100_ptx.cuh"
 
