@@ -1,6 +1,8 @@
 """moe_linear: refusals on the host, and the GPU kernels against the formula in 64 bits."""
 import ctypes
 import math
+import os
+import re
 
 import numpy as np
 import pytest
@@ -59,6 +61,24 @@ def test_python_refusals_need_no_gpu():
         api.moe_linear(torch.zeros(4, 8).bfloat16(), torch.zeros(4, 8).bfloat16())
     with pytest.raises(ValueError):
         api.moe_linear(torch.zeros(8).bfloat16(), torch.zeros(4, 8).bfloat16())
+
+
+def test_the_fit_of_gelu_s_tail():
+    # the constants as the source has them, in fp32, against exp(z^2) erfc(z) in 64 bits
+    with open(os.path.join(build.CSRC, "linear.cuh")) as f:
+        src = f.read()
+    src = src[src.index("float lin_gelu(float v)"):]
+    src = src[:src.index("}\n")]
+    f32 = lambda m: float(np.float32(m))
+    a = f32(re.search(r"fmaf\(([0-9.]+)f, fabsf\(v\)", src).group(1))
+    coefs = [f32(c) for c in re.findall(r"float p = ([-+.e0-9]+)f;", src) + re.findall(r"fmaf\(p, x, ([-+.e0-9]+)f\)", src)]
+    assert len(coefs) == 11
+    t = torch.linspace(1e-9, 1.0, 200001, dtype=torch.float64)
+    z = (1.0 / t - 1.0) / a * math.sqrt(0.5)
+    p = torch.zeros_like(t)
+    for c in coefs:
+        p = p * (2.0 * t - 1.0) + c
+    assert float((p * t / torch.special.erfcx(z) - 1.0).abs().max()) < 4.5e-8
 
 
 # ------------------------------------------------------------------ the formula in 64 bits
