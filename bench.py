@@ -169,15 +169,17 @@ def load_peaks():
         return dict(FALLBACK_PEAKS, sm_max_mhz=1965.0), "fallback"
 
 
+# what the expert GEMMs' .cu files include of kernel code
+GEMM_HEADERS = ["sm100_ptx.cuh", "warp_ptx.cuh", "pair_ptx.cuh", "row_store.cuh", "moe_internal.h"]
 STAGE_SOURCES = {
     "route": ["route.cu", "route_certified.cu", "route_common.cuh", "fp8.cu", "fp8_common.cuh", "sm100_ptx.cuh",
               "moe_internal.h"],
     "gemm_gate_up": ["grouped_gemm.cu", "grouped_gemm_2cta.cu", "fp8.cu", "fp8_swapab.cu", "fp8_common.cuh",
-                     "mx.cu", "sm100_ptx.cuh", "moe_internal.h"],
-    "gemm_down": ["grouped_gemm.cu", "grouped_gemm_2cta.cu", "fp8.cu", "fp8_common.cuh", "mx.cu", "combine.cuh",
-                  "sm100_ptx.cuh", "moe_internal.h"],
+                     "mx.cu"] + GEMM_HEADERS,
+    "gemm_down": ["grouped_gemm.cu", "grouped_gemm_2cta.cu", "fp8.cu", "fp8_common.cuh", "mx.cu",
+                  "combine.cuh"] + GEMM_HEADERS,
     "combine": ["combine.cu", "combine.cuh"],
-    "gemm_layer": ["grouped_gemm.cu", "grouped_gemm_2cta.cu", "combine.cuh", "sm100_ptx.cuh", "moe_internal.h"],
+    "gemm_layer": ["grouped_gemm.cu", "grouped_gemm_2cta.cu", "combine.cuh"] + GEMM_HEADERS,
 }
 
 

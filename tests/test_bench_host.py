@@ -4,6 +4,7 @@ clock summary.  The expected values are worked out by hand from the layer's shap
 (the per-stage formulas of the design notes) or taken from the ncu launch lists."""
 import json
 import os
+import re
 
 import pytest
 
@@ -209,3 +210,22 @@ def test_kernels_per_forward_variants():
     assert bench.kernels_per_forward(bench.WORKLOADS["mx"]) == 11   # as fp8 (T > 64: the standalone combine)
     assert bench.kernels_per_forward(bench.WORKLOADS["mx"].replace(T=16)) == 2 + 2 + 2 + 1  # no fused combine
     assert bench.kernels_per_forward(bench.WORKLOADS["prefill_shared"]) == 9   # the shared expert adds none
+
+
+def test_a_stage_s_sources_hold_the_headers_of_its_kernels():
+    # directly or by way of another header; the launch attributes of pdl.cuh and, in the stages that do not
+    # combine, the combine apart
+    def included(name, seen):
+        with open(os.path.join(bench.ROOT, "routed_grouped_gemm_softmax_b200", "csrc", name)) as f:
+            for h in re.findall(r'^#include "(\w+\.cuh)"', f.read(), re.M):
+                if h not in seen:
+                    seen.add(h)
+                    included(h, seen)
+        return seen
+
+    for stage, files in bench.STAGE_SOURCES.items():
+        seen = set()
+        for f in files:
+            included(f, seen)
+        missing = seen - set(files) - {"pdl.cuh"} - ({"combine.cuh"} if stage in ("route", "gemm_gate_up") else set())
+        assert not missing, (stage, missing)
