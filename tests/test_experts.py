@@ -517,3 +517,93 @@ def test_a_token_s_bits_depend_on_its_company_only_through_h(H, I, E, k):
     large = api.moe_experts(x, idx, w, *W)
     for T in (few + 1, 2 * few, 5 * few, 20 * few, 100 * few, n // 10, n // 3):
         assert torch.equal(api.moe_experts(x[:T], idx[:T], w[:T], *W), large[:T]), T
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,H,I,E,k", [(270000, 2048, 64, 4, 4), (270000, 64, 2048, 4, 4)])
+@pytest.mark.parametrize("pair", ["auto", "never"])
+def test_offsets_past_32_bits(T, H, I, E, k, pair):
+    # y or h of more than 2^31 elements
+    assert T * k * max(H, I) > 2 ** 31
+    x, W = rnd((T, H), 1), weights(E, H, I)
+    g = torch.Generator().manual_seed(5)
+    idx = torch.rand(T, E, generator=g).argsort(1)[:, :k].int()
+    idx[torch.rand(T, k, generator=g) < 0.01] = -1
+    idx, w = idx.cuda(), torch.randn(T, k, generator=g).cuda()
+    ws = api.experts_workspace(T, H, I, E, k, "cuda")
+    try:
+        api.set_pair_mma(pair)
+        out = api.moe_experts(x, idx, w, *W, ws=ws)
+    finally:
+        api.set_pair_mma("auto")
+    assert api.moe_get_device_status(ws) == api.MOE_OK
+    del ws
+    some = torch.cat([torch.arange(300), T - 1 - torch.arange(300), torch.randint(0, T, (2000,), generator=g)]).cuda()
+    check(out[some], x[some], idx[some], w[some], *W)
+
+
+# lists that one block groups and longer ones, experts on both sides of what it takes, several sizes
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["fp8", "mx"])
+@pytest.mark.parametrize("T,H,I,E,k", [(1, 1024, 512, 16, 8), (33, 512, 1024, 60, 5), (1200, 1024, 512, 8, 4), (4100, 512, 512, 3, 1),
+                                       (300, 512, 512, 376, 2), (300, 512, 512, 400, 2)])
+def test_quantised_forms_at_other_sizes(kind, T, H, I, E, k):
+    x, W = rnd((T, H), 1), quantised(kind, E, H, I)
+    rw = rnd((H, E), 7, 0.05)
+    idx, w = api.moe_route(x, rw, None, k)
+    ref = getattr(api, f"moe_forward_{kind}")(x, rw, None, *W, k)
+    fn = getattr(api, f"moe_experts_{kind}")
+    ws = api.experts_workspace(T, H, I, E, k, "cuda", {"fp8": 1, "mx": 2}[kind]).fill_(0xFF)
+    assert torch.equal(fn(x, idx, w, *W, ws=ws), ref) and bool((ref != 0).any())
+    g = torch.Generator().manual_seed(3)
+    gone = torch.rand(T, k, generator=g).cuda() < 0.4
+    want = fn(x, idx, torch.where(gone, 0.0, w), *W)
+    for bad in (-1, E):
+        some = fn(x, torch.where(gone, bad, idx), torch.where(gone, float("nan"), w), *W, ws=ws)
+        assert api.moe_get_device_status(ws) == (6 if bad == E and bool(gone.any()) else api.MOE_OK)
+        assert torch.equal(some, want)
+
+
+@pytest.mark.gpu
+def test_calls_from_two_threads():
+    # each thread with a stream, inputs and workspaces of its own; the library's own state is shared
+    import threading
+    from test_linear import operands
+    from test_route_scored import rows
+    cases = []
+    for n, (T, H, I, E, k) in enumerate([(5, 256, 128, 16, 4), (200, 320, 192, 8, 2), (1000, 256, 128, 32, 4)]):
+        W = weights(E, H, I)
+        idx, w = routing(T, E, k, seed=n, empty=0.1)
+        cases.append((rows(T, E, 0, torch.float32, n), rnd((T, H), n), idx, w, W, k, operands(T, 300 + 1000 * n, 256)))
+
+    def run(c, stream=None, ews=None, lws=None):
+        logits, x, idx, w, W, k, (a, b, u) = c
+        return (*api.moe_route_scored(logits, k, "sigmoid", stream=stream), api.moe_experts(x, idx, w, *W, ws=ews, stream=stream),
+                api.moe_linear(a, b, act="silu", w_up=u, ws=lws, stream=stream))
+
+    want = [run(c) for c in cases]
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(order):
+        try:
+            s = torch.cuda.Stream()
+            lws = api.linear_workspace("cuda", s)
+            ews = [api.experts_workspace(c[1].shape[0], c[1].shape[1], c[4][0].shape[1], c[4][0].shape[0], c[5], "cuda", stream=s)
+                   for c in cases]
+            got = []
+            for _ in range(30):
+                got += [(i, run(cases[i], s, ews[i], lws)) for i in order]
+            s.synchronize()
+            assert api.moe_get_device_status(lws, s) == api.MOE_OK
+            for i, outs in got:
+                assert all(torch.equal(a, b) for a, b in zip(outs, want[i])), i
+        except BaseException as e:
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(o,)) for o in ((0, 1, 2), (2, 1, 0), (1, 2, 0))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
