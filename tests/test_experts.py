@@ -607,3 +607,45 @@ def test_calls_from_two_threads():
     for t in threads:
         t.join()
     assert not failed, failed
+
+
+FIRST_CALL = """
+import sys, torch
+from routed_grouped_gemm_softmax_b200 import api
+which, T = sys.argv[1], int(sys.argv[2])
+g = torch.Generator(device="cuda").manual_seed(1)
+r = lambda *s: torch.randn(*s, generator=g, device="cuda")
+logits, x = r(T, 16), r(T, 256).bfloat16()
+W = [(r(*s) / 16).bfloat16() for s in ((16, 128, 256), (16, 128, 256), (16, 256, 128))]
+idx, w, a, b = torch.randint(0, 16, (T, 4), generator=g, device="cuda").int(), r(T, 4), r(T, 256).bfloat16(), r(2100, 256).bfloat16()
+call = {"route": lambda: api.moe_route_scored(logits, 4, "sigmoid"), "experts": lambda: (api.moe_experts(x, idx, w, *W),),
+        "linear": lambda: (api.moe_linear(a, b, act="gelu"),), "linear gated": lambda: (api.moe_linear(a, b, w_up=b),)}[which]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = call()
+for o in got:
+    o.zero_()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(o, v) and bool((o != 0).any()) for o, v in zip(got, call()))
+print("the same")
+"""
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("which", ["route", "experts", "linear", "linear gated"])
+def test_the_first_call_of_a_process_may_be_captured(which):
+    import subprocess
+    import sys
+    from conftest import ROOT
+    for T in (3, 700):
+        p = subprocess.run([sys.executable, "-c", FIRST_CALL, which, str(T)], cwd=ROOT, capture_output=True, text=True, timeout=300)
+        assert p.returncode == 0 and "the same" in p.stdout, p.stderr[-2000:]
+
+
+@pytest.mark.gpu
+def test_an_empty_batch():
+    x, W = rnd((4, 64), 1), weights(4, 64, 64)
+    idx, w = routing(4, 4, 2)
+    assert api.moe_experts(x[:0], idx[:0], w[:0], *W).shape == (0, 64)
