@@ -438,7 +438,10 @@ cudaError_t launch_pairs(const moe_linear_t &d, const void *x, const void *w, co
 // them, 10.4 on linear_kernel's; 512 x 2048 x 2048, 32 tiles: 10.8 and 10.5; 300 x 1000 x 1000, 16
 // tiles: 9.2 and 6.2).  A stage of a 256 x 256 tile takes half as long again as one of a 256 x
 // 128 tile, and the tiles run in waves of all pairs: 512 x 4096 x 4096 17.8 on 64 tiles of 128, 25.7
-// on 32 of 256; 1024 rows 30.0 and 27.4; 1500 x 4104 x 1408, 3 waves and 2, 18.1 and 20.5.
+// on 32 of 256; 1024 rows 30.0 and 27.4; 1500 x 4104 x 1408, 3 waves and 2, 18.1 and 20.5.  The rule
+// counts stages alone.  Where rows of out are not 16-byte aligned the epilogue is the longer part, and
+// the two are close: gelu with residual, 128 and 256 columns, 1001 x 4099 x 1416 25.4 and 26.4, 2001 rows
+// 45.9 and 46.5, 1024 x 4098 x 512 17.5 and 18.1.
 cudaError_t launch_linear(const moe_linear_t &d, const void *x, const void *w, const void *w_up, const LinArgs &g,
                           cudaStream_t st)
 {
