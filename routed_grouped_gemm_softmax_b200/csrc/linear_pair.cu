@@ -15,7 +15,8 @@
 // tensor map; the residual's box arrives at the same place before.  (Rows turned in shared
 // memory and stored four columns a lane took 3700 cycles a box's worth, whose latency a tile
 // that is a CTA's last does not hide: 512 x 2048 x 2048 11.6 us.)  Where rows of out or
-// residual are not 16-byte aligned a box is written row by row, a column a lane.  Tiles are
+// residual are not 16-byte aligned a box is written row by row, a column a lane, and so is the last
+// box of aligned rows whose N ends inside of a 16-byte piece.  Tiles are
 // dealt out statically, bands of 8 row tiles walked column by column, so that the
 // tiles in flight share x and w rows in L2.  Every wait is bounded.
 #include <mutex>
@@ -106,6 +107,23 @@ __device__ __forceinline__ void store_rows(const LinArgs &g, const uint8_t *from
             if (g.res) o += static_cast<float>(r[i]);
             if (FULL || r0 + i < rows) out[(r0 + i) * g.ldo] = static_cast<T>(o);
         }
+    }
+}
+
+// The box of finished values at `from`, laid out as its tensor map has it, row by row, a column a lane:
+// those inside out only.
+template <typename T>
+__device__ __forceinline__ void store_box_rows(const LinArgs &g, const uint8_t *from, int row, int col, int lane)
+{
+    constexpr int EACH = 16 / (int)sizeof(T);  // columns of a 16-byte piece
+    const int rows = min(32, g.M - row);
+    if (col + lane >= g.N) return;
+    T *out = static_cast<T *>(g.out) + (int64_t)row * g.ldo + col + lane;
+#pragma unroll 1
+    for (int r = 0; r < rows; ++r) {
+        const int swizzle = sizeof(T) == 4 ? r & 7 : r >> 1 & 3;
+        out[r * g.ldo] = *reinterpret_cast<const T *>(from + r * 32 * (int)sizeof(T) + ((lane / EACH) ^ swizzle) * 16 +
+                                                      lane % EACH * (int)sizeof(T));
     }
 }
 
@@ -306,9 +324,19 @@ __device__ __forceinline__ void pair_epilogue(const LinMaps &maps, const LinArgs
                 finish(v, u, to, h, b, bu);
             }
             if (g.maps_out) {
+                // A tensor-map store writes 16-byte pieces whole, those that the last column lies in too: up
+                // to 14 bytes behind a row of N columns.  The last box of such rows goes by plain stores.
+                const bool plain = col + j * 32 + 31 >= g.N && g.N % (g.out_f32 ? 4 : 8) != 0;
+                if (plain) {
+                    __syncwarp();
+                    if (g.out_f32)
+                        store_box_rows<float>(g, to, row, col + j * 32, lane);
+                    else
+                        store_box_rows<__nv_bfloat16>(g, to, row, col + j * 32, lane);
+                }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
-                if (lane == 0) tma_store_2d(&maps.out, to, col + j * 32, row);
+                if (lane == 0 && !plain) tma_store_2d(&maps.out, to, col + j * 32, row);
                 if (res_maps && turns == 1) load_next(i, j, count, row, col);
             } else {
                 __syncwarp();

@@ -373,3 +373,25 @@ def test_one_column_whose_gate_and_up_rows_lie_apart(M):
     x, w, u = mat(M, 64, 1), mat(1, 64, 2, 24), mat(1, 64, 3)
     check(x, w, None, "silu", None, u)
     check(x, u, None, "silu", None, w)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,K", [(1000, 72), (257, 1100), (2600, 40)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_columns_behind_rows_that_end_inside_16_bytes(M, K, dtype):
+    # rows 16-byte aligned, N any: out a slice of a wider buffer whose other columns stay as they were,
+    # down to the last row's, behind which a buffer may end
+    for N in (2043, 2044, 2045, 2046, 2047, 2049, 2050, 2082, 4100):
+        x, w, u = operands(M, N, K)
+        b = mat(1, N, 4, dtype=torch.float32)[0]
+        pad = (-N) % 8 + 8
+        for gate, act, res in ((None, "gelu", None), (u, "silu", None), (None, "none", "apart"), (u, "relu", "in place")):
+            big = torch.full((M + 1, N + pad), 7.0, dtype=dtype, device="cuda")
+            out, r = big[:M, :N], None
+            if res == "apart":
+                r = mat(M, N, 8, pad, dtype)
+            elif res:
+                out.copy_(mat(M, N, 9, 0, dtype))
+                r = out
+            check(x, w, b, act, r, gate, out_dtype=dtype, out=out)
+            assert bool((big[M:] == 7.0).all()) and bool((big[:, N:] == 7.0).all()), (N, gate is not None, res)
