@@ -33,8 +33,9 @@ constexpr int LKC = 2;  // 64-column chunks of a stage: 256 contiguous bytes a r
 
 // A CTA may wait in tcgen05.alloc for what others hold, while those wait for their clusters: no such
 // ring closes as long as all that fit an SM at once have their columns. Registers admit 7 CTAs
-// of 64 columns (48 registers a thread, tiles of 16), 5 of 64 or 3 of 128 (102), below 512 in all; a
-// kernel of 512 columns leaves no shared memory for a CTA of this one beside it.
+// of 64 columns (48 registers a thread, tiles of 16), 5 of 64 or 3 of 128 (102), below 512 in all.  The
+// kernels of 256 or 512 columns leave no shared memory for a CTA of this one beside them, but for the MX
+// GEMM, whose CTAs wait for no other block.
 
 // Rows of a tile that each of `split` CTAs finishes.
 __host__ __device__ __forceinline__ int lin_own(int bn, int split) { return (bn + split - 1) / split; }
